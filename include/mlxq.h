@@ -235,6 +235,76 @@ MLXQ_API int mlxq_dequant_as(const mlxq_weight* w, void* out, int dtype, uint64_
 MLXQ_API int mlxq_quantize(const void* w_bf16, const mlxq_weight* dst, uint64_t stream);
 
 /*
+ * MX4: microscaled 4-bit floating point (no page entry; the model pages name
+ * 4-bit weights without giving a format, so the open microscaling one is used).
+ *   codes   uint32 [rows, cols/8], row-major: eight E2M1 codes per word, the low
+ *           nibble is the first column.  A code is sign (bit 3), exponent (2
+ *           bits), mantissa (1 bit): 0, .5, 1, 1.5, 2, 3, 4, 6 and negatives.
+ *   scales  uint8 [rows, cols/32], E8M0: 2^(byte - 127), 255 is NaN.
+ *   Element: W[n,k] = E2M1(code[n,k]) * 2^(scales[n,k/32] - 127).
+ * The handle does not own its buffers (device memory of the current device;
+ * codes 16-byte, scales 4-byte aligned); cols is a multiple of 32.  The same
+ * format holds weights and quantized activations.
+ */
+typedef struct mlxq_mx4 {
+    void* codes;
+    void* scales;
+    uint32_t rows;
+    uint32_t cols;
+} mlxq_mx4;
+
+/*
+ * mlxq_mx4_quantize.  x_bf16: BF16 [rows, cols] row-major, device.  Per block of
+ * 32 columns with m = max |x|:  e = clamp(floor(log2 m) - 2, -127, 127), scale
+ * byte e + 127, code = the E2M1 value nearest to x 2^-e (ties to the even code,
+ * magnitudes above 6 to 6).  A block of zeros has scale byte 0; a block that
+ * holds an infinity or a NaN has scale byte 255 and codes 0 (it reads as NaN).
+ */
+MLXQ_API int mlxq_mx4_quantize(const void* x_bf16, const mlxq_mx4* dst, uint64_t stream);
+
+/* mlxq_mx4_dequant.  Writes the elements as BF16 [rows, cols] to `out`; exact
+ * unless an element overflows (to infinity). */
+MLXQ_API int mlxq_mx4_dequant(const mlxq_mx4* w, void* out, uint64_t stream);
+
+/*
+ * mlxq_mx4_gemm.  Y = X W^T with BF16 activations (weight-only).  X: BF16
+ * [m, cols] row-major, 16-byte aligned; Y: BF16 [m, rows].  0 <= m <= 64 (m == 0
+ * is a no-op; more rows: MLXQ_ERR_UNSUPPORTED, see mlxq_mx4_matmul).
+ */
+MLXQ_API int mlxq_mx4_gemm(const mlxq_mx4* w, const void* x, void* y, uint32_t m, uint64_t stream);
+
+/*
+ * A mixture-of-experts layer for 0 <= m <= 64 tokens:
+ *   logits = x R^T;  S[t] = the top_k largest of token t (ties: lowest index);
+ *   p = softmax over S[t], or over all experts with MLXQ_MOE_SOFTMAX_ALL;
+ *   y[t] = sum over e in S[t] of  Wd_e ( p_e silu(Wg_e x[t]) * (Wu_e x[t]) ).
+ * router: BF16 [experts, hidden]; x, y: BF16 [m, hidden] (router and x 16-byte
+ * aligned).  The experts' weights are stacked: gate and up have experts * inter
+ * rows of hidden columns, down experts * hidden rows of inter columns; rows of
+ * expert e follow those of expert e - 1.  1 <= experts <= 256, 1 <= top_k <=
+ * min(experts, 16).  The gated product is rounded once, to BF16, before the down
+ * projection; all sums are fp32.
+ *   mlxq_moe      8-bit weights; hidden and inter multiples of 64, group_size 32,
+ *                 64 or 128 (one for gate and up), codes 16-byte and tables
+ *                 4-byte aligned.  Weight flags are ignored.
+ *   mlxq_mx4_moe  MX4 weights; hidden and inter multiples of 32.
+ * workspace: device memory, 16-byte aligned, of at least
+ * mlxq_moe_workspace_bytes bytes; its contents on entry do not matter.  One call
+ * at a time may use it: calls (and captured graphs) that can overlap on the GPU
+ * need a workspace each.  The call is two kernel launches, the second a
+ * cooperative one, which is refused (MLXQ_ERR_CUDA) where the device cannot
+ * hold one block per SM at once.
+ */
+#define MLXQ_MOE_SOFTMAX_ALL 1u
+MLXQ_API size_t mlxq_moe_workspace_bytes(uint32_t hidden, uint32_t inter, uint32_t top_k, uint32_t m);
+MLXQ_API int mlxq_moe(const void* router, const mlxq_weight* gate, const mlxq_weight* up, const mlxq_weight* down,
+             uint32_t experts, uint32_t top_k, uint32_t flags, const void* x, void* y, uint32_t m, void* workspace,
+             size_t workspace_bytes, uint64_t stream);
+MLXQ_API int mlxq_mx4_moe(const void* router, const mlxq_mx4* gate, const mlxq_mx4* up, const mlxq_mx4* down,
+             uint32_t experts, uint32_t top_k, uint32_t flags, const void* x, void* y, uint32_t m, void* workspace,
+             size_t workspace_bytes, uint64_t stream);
+
+/*
  * Self-tests of the failure paths (no page entry; used by the tests).
  *
  * mlxq_selftest_wait_timeout: launches one warp on `stream` that waits,

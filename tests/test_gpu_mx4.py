@@ -1,0 +1,221 @@
+"""GPU parity of the MX4 calls against a plain 64-bit reference: quantisation and
+dequantisation bit for bit, products within a bound derived from their sums."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import _mx4_ref as ref
+import synth
+import weight_only_quantized_mlx_b200 as mq
+from _helpers import Guarded, bits_to_f64, dev, host_bits
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    mq.lib()
+    yield
+    torch.cuda.synchronize()
+    mq.mlxq_device_status()
+
+
+def padded(nbytes):
+    """A byte buffer in the middle of guard bytes: (whole, view)."""
+    b = torch.full((nbytes + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    return b, b[256:256 + nbytes]
+
+
+def check_pads(b, nbytes):
+    h = b.cpu().numpy()
+    assert np.all(h[:256] == 0xA5) and np.all(h[256 + nbytes:] == 0xA5), "write outside the buffer"
+
+
+def run_quantize(bits, offset=0):
+    rows, cols = bits.shape
+    src = torch.zeros(rows * cols + offset, dtype=torch.bfloat16, device="cuda")
+    src[offset:] = dev(bits).reshape(-1)
+    cb, codes = padded(rows * cols // 2)
+    sb, scales = padded(rows * cols // 32)
+    mq.mlxq_mx4_quantize(src[offset:], mq.mlxq_mx4(codes.data_ptr(), scales.data_ptr(), rows, cols))
+    torch.cuda.synchronize()
+    check_pads(cb, rows * cols // 2)
+    check_pads(sb, rows * cols // 32)
+    return codes.cpu().numpy().view(np.uint32).reshape(rows, -1), scales.cpu().numpy().reshape(rows, -1)
+
+
+def draw(kind, g, rows, cols):
+    if kind == "normal":
+        return synth.activations(g, rows, cols)
+    if kind == "bits":  # every exponent, finite
+        b = g.integers(0, 1 << 16, (rows, cols)).astype(np.uint16)
+        return np.where((b & 0x7F80) == 0x7F80, b & 0xBFFF, b).astype(np.uint16)
+    if kind == "ties":  # borders of the grid at several scales
+        v = g.choice([0, .25, .5, .75, 1, 1.25, 1.5, 1.75, 2, 2.5, 3, 3.5, 4, 5, 6, 7], (rows, cols)) * g.choice([-1, 1], (rows, cols))
+        return synth.to_bf16_bits(v * 2.0 ** g.integers(-140, 120, (rows, 1)))
+    if kind == "tiny":  # zeros of both signs, subnormals, the smallest normals
+        return (g.choice([0, 0, 1, 2, 3, 0x40, 0x7F, 0x80, 0xC0, 0x17F, 0x1FF], (rows, cols)) | (g.integers(0, 2, (rows, cols)) << 15)).astype(np.uint16)
+    b = synth.activations(g, rows, cols)  # "special": some blocks hold infinities and NaN
+    b[0, 0], b[-1, -1], b[0, cols // 2] = 0x7F80, 0xFFC0, 0xFF80
+    return b
+
+
+@pytest.mark.parametrize("kind", ["normal", "bits", "ties", "tiny", "special"])
+@pytest.mark.parametrize("rows,cols", [(1, 32), (1, 4096), (3, 96), (67, 160), (33, 1056)])
+def test_quantize_bit_exact(rows, cols, kind):
+    bits = draw(kind, synth.rng(rows + cols), rows, cols)
+    want_codes, want_scales = ref.quantize(bits)
+    for offset in (0, 1, 8):  # 32-byte aligned, 2-byte, 16-byte
+        codes, scales = run_quantize(bits, offset)
+        assert np.array_equal(scales, want_scales), offset
+        assert np.array_equal(codes, ref.pack(want_codes)), offset
+
+
+def test_dequant_every_code_and_scale_bit_exact():
+    codes = np.tile(np.arange(16, dtype=np.uint8), (256, 4))  # 64 columns: two blocks
+    scales = np.stack([np.arange(256), 255 - np.arange(256)], axis=1).astype(np.uint8)
+    want = ref.values(codes, scales)
+    with np.errstate(over="ignore", invalid="ignore"):
+        want_bits = synth.to_bf16_bits(want.astype(np.float32))  # exact, or infinite
+    for offset in (0, 1, 8):
+        out = Guarded(codes.size, offset_elems=offset)
+        h = mq.mx4_view(dev(ref.pack(codes)), dev(scales))
+        mq.mlxq_mx4_dequant(h, out.data_ptr())
+        torch.cuda.synchronize()
+        out.check_guards()
+        got = out.value_bits().reshape(codes.shape)
+        nan = np.isnan(want)
+        assert np.array_equal(np.isnan(bits_to_f64(got)), nan)
+        assert np.array_equal(got[~nan], want_bits[~nan])
+
+
+def bound(absw, absx, y, K):
+    """|Y - Y_ref| for an fp32 sum of K exact products on the tensor pipe (each of
+    its K / 16 steps loses at most 2^-22 of the sum of magnitudes, the joins of
+    partial sums a few more), rounded once to BF16."""
+    s = (K / 16 + 32) * 2.0 ** -22 * (absx @ absw.T)
+    return s + 2.0 ** -8 * (np.abs(y) + s)
+
+
+def make(seed, rows, cols, **k):
+    g = synth.rng(seed)
+    codes, scales = ref.random_weight(g, rows, cols, **k)
+    return g, codes, scales, mq.mx4_view(dev(ref.pack(codes)), dev(scales))
+
+
+GEMM = [(1, 1, 32), (1, 9, 64), (3, 148, 96), (8, 300, 4128), (9, 17, 160), (16, 4099, 544), (17, 1200, 128),
+        (33, 2500, 1056), (64, 333, 2080), (61, 64, 32), (1, 4096, 4096), (5, 9000, 256), (40, 5003, 96)]
+
+
+@pytest.mark.parametrize("m,N,K", GEMM)
+def test_gemm(m, N, K):
+    g, codes, scales, h = make(m + N, N, K)
+    w = ref.values(codes, scales)
+    xb = synth.activations(g, m, K)
+    x = bits_to_f64(xb)
+    y = Guarded(m * N)
+    mq.mlxq_mx4_gemm(h, dev(xb), y.data_ptr(), m)
+    torch.cuda.synchronize()
+    y.check_guards()
+    want = x @ w.T
+    err = np.abs(bits_to_f64(y.value_bits()).reshape(m, N) - want)
+    assert np.all(err <= bound(np.abs(w), np.abs(x), want, K)), float(err.max())
+
+
+@pytest.mark.parametrize("m", [1, 12])
+def test_gemm_extreme_scales(m):
+    """Scale bytes from 0 to 254, mixed within rows; x small enough that nothing overflows."""
+    N, K = 70, 416
+    g, codes, scales, h = make(5, N, K, low=100, high=150)
+    scales[:, 0], scales[:, 1], scales[:, 2] = 0, 128, 129
+    scales[3, :] = 250
+    h = mq.mx4_view(dev(ref.pack(codes)), dev(scales))
+    w = ref.values(codes, scales)
+    xb = synth.to_bf16_bits(g.standard_normal((m, K)) * 2.0 ** -20)
+    x = bits_to_f64(xb)
+    y = torch.empty(m, N, dtype=torch.bfloat16, device="cuda")
+    mq.mlxq_mx4_gemm(h, dev(xb), y, m)
+    want = x @ w.T
+    err = np.abs(bits_to_f64(host_bits(y)) - want)
+    assert np.all(err <= bound(np.abs(w), np.abs(x), want, K))
+
+
+@pytest.mark.parametrize("m", [2, 20])
+def test_gemm_nan_and_infinity_stay_in_their_rows(m):
+    N, K = 40, 224
+    g, codes, scales, h = make(6, N, K)
+    scales[7, 6] = 255
+    h = mq.mx4_view(dev(ref.pack(codes)), dev(scales))
+    xb = synth.activations(g, m, K)
+    xb[1, K - 1] = 0x7FC0
+    y = torch.empty(m, N, dtype=torch.bfloat16, device="cuda")
+    mq.mlxq_mx4_gemm(h, dev(xb), y, m)
+    nan = np.isnan(bits_to_f64(host_bits(y)))
+    want = np.zeros((m, N), bool)
+    want[1, :], want[:, 7] = True, True
+    assert np.array_equal(nan, want)
+
+
+def test_gemm_of_no_columns_is_zero_and_empty_outputs_are_nothing():
+    y = torch.full((2, 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    mq.mlxq_mx4_gemm(mq.mlxq_mx4(None, None, 8, 0), None, y, 2)
+    assert not y.any()
+    mq.mlxq_mx4_gemm(mq.mlxq_mx4(None, None, 0, 64), torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda"), None, 2)
+    mq.mlxq_mx4_quantize(None, mq.mlxq_mx4(None, None, 0, 64))
+    mq.mlxq_mx4_dequant(mq.mlxq_mx4(None, None, 3, 0), None)
+    torch.cuda.synchronize()
+
+
+def test_quantize_then_gemm_on_a_side_stream_and_in_a_graph():
+    """The calls in a row as a program makes them, on a stream of its own, captured and replayed."""
+    rows, cols, m = 200, 256, 4
+    g = synth.rng(9)
+    wb, xb = synth.activations(g, rows, cols), synth.activations(g, m, cols)
+    w, x = dev(wb), dev(xb)
+    q = mq.mx4_empty(rows, cols)
+    back = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty(m, rows, dtype=torch.bfloat16, device="cuda")
+
+    def chain(s):
+        mq.mlxq_mx4_quantize(w, q, s)
+        mq.mlxq_mx4_dequant(q, back, s)
+        mq.mlxq_mx4_gemm(q, x, y, m, s)
+
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    chain(s)
+    s.synchronize()
+    eager, eager_back = host_bits(y), host_bits(back)
+    v = ref.values(*ref.quantize(wb))
+    assert np.array_equal(bits_to_f64(eager_back), v)
+    xv = bits_to_f64(xb)
+    assert np.all(np.abs(bits_to_f64(eager) - xv @ v.T) <= bound(np.abs(v), np.abs(xv), xv @ v.T, cols))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        chain(s)
+    y.zero_()
+    back.zero_()
+    q.tensors[0].zero_()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(host_bits(y), eager) and np.array_equal(host_bits(back), eager_back)
+
+
+def test_gemm_past_32_bits_of_codes():
+    """A weight whose codes pass 2^31 bytes: the last rows are read where they are."""
+    N, K = 2 ** 20 + 8, 4224
+    codes = torch.zeros(N, K // 8, dtype=torch.int32, device="cuda")
+    scales = torch.full((N, K // 32), 127, dtype=torch.uint8, device="cuda")
+    codes[-1] = 0x22222222      # ones
+    codes[N // 2] = 0x44444444  # twos
+    x = torch.ones(1, K, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty(1, N, dtype=torch.bfloat16, device="cuda")
+    mq.mlxq_mx4_gemm(mq.mx4_view(codes, scales), x, y, 1)
+    want = torch.zeros(N, dtype=torch.bfloat16, device="cuda")
+    want[-1], want[N // 2] = K, 2 * K
+    assert torch.equal(y[0], want)

@@ -40,6 +40,8 @@ MLXQ_GEMM_SMALLM_TC = 6
 
 MLXQ_WEIGHT_STATIC = 1
 
+MLXQ_MOE_SOFTMAX_ALL = 1
+
 MLXQ_DTYPE_BF16 = 0
 MLXQ_DTYPE_F16 = 1
 MLXQ_DTYPE_F32 = 2
@@ -47,7 +49,8 @@ MLXQ_DTYPE_F32 = 2
 EXPORTS = ("mlxq_load", "mlxq_dequant", "mlxq_gemv", "mlxq_gemv_silu_gate",
            "mlxq_gemv_silu_gate_resid", "mlxq_gemm", "mlxq_gemm_with", "mlxq_gemm_noalloc", "mlxq_release",
            "mlxq_last_error", "mlxq_device_status", "mlxq_dequant_as", "mlxq_quantize", "mlxq_selftest_wait_timeout",
-           "mlxq_selftest_fail_alloc")
+           "mlxq_selftest_fail_alloc", "mlxq_mx4_quantize", "mlxq_mx4_dequant", "mlxq_mx4_gemm",
+           "mlxq_moe_workspace_bytes", "mlxq_moe", "mlxq_mx4_moe")
 
 
 class mlxq_weight(ctypes.Structure):
@@ -56,6 +59,14 @@ class mlxq_weight(ctypes.Structure):
                 ("biases", ctypes.c_void_p), ("out_features", ctypes.c_uint32),
                 ("in_features", ctypes.c_uint32), ("group_size", ctypes.c_uint32),
                 ("flags", ctypes.c_uint32)]
+
+
+class mlxq_mx4(ctypes.Structure):
+    """C ``mlxq_mx4``: codes and scales of an MX4 matrix.  A handle made by
+    :func:`mx4_view` or :func:`mx4_empty` keeps its tensors alive (``tensors``)."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("rows", ctypes.c_uint32), ("cols", ctypes.c_uint32)]
+    tensors = None
 
 
 class MlxqError(RuntimeError):
@@ -74,6 +85,7 @@ def lib() -> ctypes.CDLL:
             raise ImportError(f"{LIB_PATH} is not built; run python -m weight_only_quantized_mlx_b200.build")
         L = ctypes.CDLL(LIB_PATH)
         W = ctypes.POINTER(mlxq_weight)
+        Q = ctypes.POINTER(mlxq_mx4)
         vp, u64, u32, i32 = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_int
         sigs = {
             "mlxq_load": [ctypes.c_char_p, ctypes.c_size_t, ctypes.c_char_p, u32, W],
@@ -91,11 +103,18 @@ def lib() -> ctypes.CDLL:
             "mlxq_dequant_as": [W, vp, i32, u64],
             "mlxq_selftest_wait_timeout": [u32, u64],
             "mlxq_selftest_fail_alloc": [u32],
+            "mlxq_mx4_quantize": [vp, Q, u64],
+            "mlxq_mx4_dequant": [Q, vp, u64],
+            "mlxq_mx4_gemm": [Q, vp, vp, u32, u64],
+            "mlxq_moe_workspace_bytes": [u32, u32, u32, u32],
+            "mlxq_moe": [vp, W, W, W, u32, u32, u32, vp, vp, u32, vp, ctypes.c_size_t, u64],
+            "mlxq_mx4_moe": [vp, Q, Q, Q, u32, u32, u32, vp, vp, u32, vp, ctypes.c_size_t, u64],
         }
+        returns = {"mlxq_last_error": ctypes.c_char_p, "mlxq_moe_workspace_bytes": ctypes.c_size_t}
         for name, args in sigs.items():
             fn = getattr(L, name)
             fn.argtypes = args
-            fn.restype = ctypes.c_char_p if name == "mlxq_last_error" else ctypes.c_int
+            fn.restype = returns.get(name, ctypes.c_int)
         _lib = L
     return _lib
 
@@ -115,6 +134,17 @@ def _stream(s) -> int:
     if isinstance(s, int):
         return s
     return s.cuda_stream
+
+
+def _dense(b, dtype: str, name: str, elems: int):
+    """The address of a buffer that holds `elems` contiguous elements of a torch
+    dtype; raw addresses are taken as they are."""
+    if b is None or isinstance(b, int):
+        return b
+    if str(b.dtype) != "torch." + dtype or not b.is_contiguous() or b.numel() < elems:
+        raise MlxqError(MLXQ_ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} tensor of at least {elems} elements, "
+                                              f"got {b.dtype} {tuple(b.shape)} with strides {tuple(b.stride())}")
+    return b.data_ptr()
 
 
 def _check(rc: int) -> None:
@@ -194,6 +224,69 @@ def weight_view(packed, scales, biases, group_size: int, flags: int = 0) -> mlxq
     N = packed.shape[0]
     K = packed.shape[1] * 4
     return mlxq_weight(_ptr(packed), _ptr(scales), _ptr(biases), N, K, group_size, flags)
+
+
+def mx4_view(codes, scales) -> mlxq_mx4:
+    """A handle over device tensors: codes (u)int32 [rows, cols/8], scales uint8
+    [rows, cols/32], both contiguous."""
+    if codes.dim() != 2 or scales.dim() != 2 or codes.element_size() != 4 or scales.element_size() != 1 \
+            or tuple(scales.shape) != (codes.shape[0], codes.shape[1] // 4) or codes.shape[1] % 4:
+        raise MlxqError(MLXQ_ERR_SHAPE, f"MX4 codes must be 32-bit [rows, cols/8] and scales 8-bit [rows, cols/32], got "
+                                        f"{tuple(codes.shape)} and {tuple(scales.shape)}")
+    if not codes.is_contiguous() or not scales.is_contiguous():
+        raise MlxqError(MLXQ_ERR_INVALID_ARG, "MX4 codes and scales must be contiguous")
+    h = mlxq_mx4(_ptr(codes), _ptr(scales), codes.shape[0], codes.shape[1] * 8)
+    h.tensors = (codes, scales)
+    return h
+
+
+def mx4_empty(rows: int, cols: int, device="cuda") -> mlxq_mx4:
+    """A handle over new, unfilled tensors, as a destination of mlxq_mx4_quantize."""
+    import torch
+    if cols % 32:
+        raise MlxqError(MLXQ_ERR_SHAPE, f"cols {cols} is not a multiple of 32")
+    return mx4_view(torch.empty(rows, cols // 8, dtype=torch.int32, device=device),
+                    torch.empty(rows, cols // 32, dtype=torch.uint8, device=device))
+
+
+def mlxq_mx4_quantize(x_bf16, dst: mlxq_mx4, stream=None) -> None:
+    x = _dense(x_bf16, "bfloat16", "x", dst.rows * dst.cols)
+    _check(lib().mlxq_mx4_quantize(x, ctypes.byref(dst), _stream(stream)))
+
+
+def mlxq_mx4_dequant(w: mlxq_mx4, out, stream=None) -> None:
+    out = _dense(out, "bfloat16", "out", w.rows * w.cols)
+    _check(lib().mlxq_mx4_dequant(ctypes.byref(w), out, _stream(stream)))
+
+
+def mlxq_mx4_gemm(w: mlxq_mx4, x, y, m: int, stream=None) -> None:
+    x, y = _dense(x, "bfloat16", "X", m * w.cols), _dense(y, "bfloat16", "Y", m * w.rows)
+    _check(lib().mlxq_mx4_gemm(ctypes.byref(w), x, y, m, _stream(stream)))
+
+
+def mlxq_moe_workspace_bytes(hidden: int, inter: int, top_k: int, m: int) -> int:
+    return lib().mlxq_moe_workspace_bytes(hidden, inter, top_k, m)
+
+
+def _moe(fn, hidden, router, gate, up, down, experts, top_k, x, y, m, workspace, stream, flags):
+    router = _dense(router, "bfloat16", "router", experts * hidden)
+    x, y = _dense(x, "bfloat16", "x", m * hidden), _dense(y, "bfloat16", "y", m * hidden)
+    if not hasattr(workspace, "data_ptr") or not workspace.is_contiguous():
+        raise MlxqError(MLXQ_ERR_INVALID_ARG, "workspace must be a contiguous tensor")
+    _check(fn(router, ctypes.byref(gate), ctypes.byref(up), ctypes.byref(down), experts, top_k, flags, x, y, m,
+              workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def mlxq_moe(router, gate: mlxq_weight, up: mlxq_weight, down: mlxq_weight, experts: int, top_k: int, x, y, m: int,
+             workspace, stream=None, flags: int = 0) -> None:
+    """workspace: a device tensor of at least mlxq_moe_workspace_bytes(...) bytes, for one call at a time."""
+    _moe(lib().mlxq_moe, gate.in_features, router, gate, up, down, experts, top_k, x, y, m, workspace, stream, flags)
+
+
+def mlxq_mx4_moe(router, gate: mlxq_mx4, up: mlxq_mx4, down: mlxq_mx4, experts: int, top_k: int, x, y, m: int,
+                 workspace, stream=None, flags: int = 0) -> None:
+    """workspace: a device tensor of at least mlxq_moe_workspace_bytes(...) bytes, for one call at a time."""
+    _moe(lib().mlxq_mx4_moe, gate.cols, router, gate, up, down, experts, top_k, x, y, m, workspace, stream, flags)
 
 
 class MlxInt8Weight:

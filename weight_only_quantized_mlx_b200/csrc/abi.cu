@@ -377,6 +377,92 @@ int check_out_vs_weight(const void* out, int64_t obytes, const WeightView& v) {
     return MLXQ_OK;
 }
 
+int check_mx4(const mlxq_mx4* w, Mx4View& v, const char* name) {
+    if (!w) return fail(MLXQ_ERR_INVALID_ARG, "null MX4 handle (%s)", name);
+    v.rows = w->rows;
+    v.cols = w->cols;
+    if (v.cols % 32 != 0) return fail(MLXQ_ERR_SHAPE, "%s: cols %u is not a multiple of 32", name, w->cols);
+    if (static_cast<uint64_t>(w->rows) * w->cols > (1ull << 50)) return fail(MLXQ_ERR_SHAPE, "%s: rows x cols is beyond any device", name);
+    if (v.rows != 0 && v.cols != 0) {
+        if (!w->codes || !w->scales) return fail(MLXQ_ERR_INVALID_ARG, "%s: codes or scales are null", name);
+        if (!aligned(w->codes, 16) || !aligned(w->scales, 4))
+            return fail(MLXQ_ERR_INVALID_ARG, "%s: codes must be 16-byte and scales 4-byte aligned", name);
+    }
+    v.codes = static_cast<const uint8_t*>(w->codes);
+    v.scales = static_cast<const uint8_t*>(w->scales);
+    return MLXQ_OK;
+}
+
+// the largest dimension of the MX4 products (32-bit row and column indexes)
+constexpr int64_t kMaxDim = int64_t{1} << 30;
+
+bool overlaps_mx4(const void* p, int64_t bytes, const Mx4View& v) {
+    return overlap(p, bytes, v.codes, v.rows * v.cols / 2) || overlap(p, bytes, v.scales, v.rows * v.cols / 32);
+}
+
+// ---- expert-layer checks ----------------------------------------------------------------------
+constexpr int64_t kMoeMaxDim = int64_t{1} << 20;
+
+// Shapes that both formats share: gate and up [E * I, H], down [E * H, I].
+int check_moe_shapes(int64_t gate_rows, int64_t gate_cols, int64_t up_rows, int64_t up_cols, int64_t down_rows, int64_t down_cols,
+                     uint32_t experts, uint32_t top_k, uint32_t flags, uint32_t m, int64_t step, MoeCall& c) {
+    if (experts == 0 || experts > static_cast<uint32_t>(kMoeMaxExperts))
+        return fail(MLXQ_ERR_UNSUPPORTED, "experts must be in [1, %d], got %u", kMoeMaxExperts, experts);
+    if (top_k == 0 || top_k > experts || top_k > static_cast<uint32_t>(kMoeMaxTopK))
+        return fail(MLXQ_ERR_UNSUPPORTED, "top_k must be in [1, min(experts, %d)], got %u", kMoeMaxTopK, top_k);
+    if (m > static_cast<uint32_t>(kMoeMaxTokens))
+        return fail(MLXQ_ERR_UNSUPPORTED, "the expert layer takes up to %d tokens (got %u)", kMoeMaxTokens, m);
+    if (flags & ~MLXQ_MOE_SOFTMAX_ALL) return fail(MLXQ_ERR_INVALID_ARG, "unknown expert-layer flags 0x%x", flags);
+    const int64_t H = gate_cols, I = down_cols;
+    if (up_rows != gate_rows || up_cols != H || gate_rows != static_cast<int64_t>(experts) * I ||
+        down_rows != static_cast<int64_t>(experts) * H)
+        return fail(MLXQ_ERR_SHAPE, "gate and up must be [experts * inter, hidden] and down [experts * hidden, inter]");
+    if (H == 0 || I == 0 || H % step != 0 || I % step != 0 || H > kMoeMaxDim || I > kMoeMaxDim)
+        return fail(MLXQ_ERR_UNSUPPORTED, "hidden and inter must be multiples of %lld, up to 2^20 (got %lld, %lld)",
+                    static_cast<long long>(step), static_cast<long long>(H), static_cast<long long>(I));
+    c.experts = static_cast<int>(experts);
+    c.top_k = static_cast<int>(top_k);
+    c.hidden = static_cast<int>(H);
+    c.inter = static_cast<int>(I);
+    c.m = static_cast<int>(m);
+    c.softmax_all = (flags & MLXQ_MOE_SOFTMAX_ALL) ? 1 : 0;
+    return MLXQ_OK;
+}
+
+// Buffers that both formats share.  `hits(p, bytes)`: whether [p, p + bytes) overlaps an expert weight.
+template <class Hits>
+int check_moe_buffers(const void* router, const void* x, void* y, void* ws, size_t ws_bytes, MoeCall& c, Hits hits) {
+    const int64_t xb = int64_t{2} * c.m * c.hidden, rb = int64_t{2} * c.experts * c.hidden;
+    int rc;
+    if ((rc = check_buf(router, rb, "router"))) return rc;
+    if ((rc = check_buf(x, xb, "x"))) return rc;
+    if ((rc = check_buf(y, xb, "y"))) return rc;
+    if (!aligned(router, 16) || !aligned(x, 16)) return fail(MLXQ_ERR_INVALID_ARG, "router and x must be 16-byte aligned");
+    const size_t need = moe_workspace_bytes(c.inter, static_cast<int64_t>(c.m) * c.top_k);
+    if (!ws || !aligned(ws, 16)) return fail(MLXQ_ERR_INVALID_ARG, "workspace is null or not 16-byte aligned");
+    if (ws_bytes < need)
+        return fail(MLXQ_ERR_INVALID_ARG, "workspace holds %zu bytes, the call needs %zu", ws_bytes, need);
+    const int64_t nb = static_cast<int64_t>(need);
+    if (overlap(y, xb, x, xb) || overlap(y, xb, router, rb) || hits(y, xb))
+        return fail(MLXQ_ERR_INVALID_ARG, "y overlaps an input");
+    if (overlap(ws, nb, x, xb) || overlap(ws, nb, y, xb) || overlap(ws, nb, router, rb) || hits(ws, nb))
+        return fail(MLXQ_ERR_INVALID_ARG, "the workspace overlaps another buffer");
+    c.router = router;
+    c.x = x;
+    c.y = y;
+    c.workspace = ws;
+    return MLXQ_OK;
+}
+
+int check_moe_weight(const WeightView& v, const char* name) {
+    if (v.gs != 32 && v.gs != 64 && v.gs != 128)
+        return fail(MLXQ_ERR_UNSUPPORTED, "%s: the expert layer takes group sizes 32, 64 and 128 (got %lld)", name,
+                    static_cast<long long>(v.gs));
+    if (!aligned(v.packed, 16) || !aligned(v.scales, 4) || !aligned(v.biases, 4))
+        return fail(MLXQ_ERR_INVALID_ARG, "%s: codes must be 16-byte and scales and biases 4-byte aligned", name);
+    return MLXQ_OK;
+}
+
 int launch_status(cudaError_t e, const char* what) {
     if (e != cudaSuccess) return fail(MLXQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
     return MLXQ_OK;
@@ -684,6 +770,87 @@ int mlxq_gemm(const mlxq_weight* w, const void* x, void* y, uint32_t m, uint64_t
 
 int mlxq_gemm_noalloc(const mlxq_weight* w, const void* x, void* y, uint32_t m, uint64_t stream) {
     return gemm_impl(w, x, y, m, MLXQ_GEMM_AUTO, stream, TC_SCRATCH_STATIC);
+}
+
+// ---- MX4 ---------------------------------------------------------------------------------
+int mlxq_mx4_quantize(const void* x_bf16, const mlxq_mx4* dst, uint64_t stream) {
+    Mx4View v;
+    int rc = check_mx4(dst, v, "dst");
+    if (rc) return rc;
+    if ((rc = check_buf(x_bf16, v.rows * v.cols, "x"))) return rc;
+    if (overlaps_mx4(x_bf16, v.rows * v.cols * 2, v) ||
+        overlap(v.codes, v.rows * v.cols / 2, v.scales, v.rows * v.cols / 32))
+        return fail(MLXQ_ERR_INVALID_ARG, "MX4 quantize source and destination buffers overlap");
+    return launch_status(launch_mx4_quantize(x_bf16, v, as_stream(stream)), "MX4 quantize launch");
+}
+
+int mlxq_mx4_dequant(const mlxq_mx4* w, void* out, uint64_t stream) {
+    Mx4View v;
+    int rc = check_mx4(w, v, "w");
+    if (rc) return rc;
+    if ((rc = check_buf(out, v.rows * v.cols, "out"))) return rc;
+    if (overlaps_mx4(out, v.rows * v.cols * 2, v)) return fail(MLXQ_ERR_INVALID_ARG, "output overlaps the weight buffers");
+    return launch_status(launch_mx4_dequant(v, out, as_stream(stream)), "MX4 dequant launch");
+}
+
+int mlxq_mx4_gemm(const mlxq_mx4* w, const void* x, void* y, uint32_t m, uint64_t stream) {
+    Mx4View v;
+    int rc = check_mx4(w, v, "w");
+    if (rc) return rc;
+    if (m > static_cast<uint32_t>(kMx4GemmMaxM))
+        return fail(MLXQ_ERR_UNSUPPORTED, "MX4 gemm with BF16 activations takes up to %d rows (got %u); quantize them and use "
+                    "mlxq_mx4_matmul for more", kMx4GemmMaxM, m);
+    if (v.rows > kMaxDim || v.cols > kMaxDim) return fail(MLXQ_ERR_UNSUPPORTED, "MX4 gemm: a dimension is beyond 2^30");
+    const int64_t M = m;
+    if ((rc = check_buf(x, M * v.cols, "X"))) return rc;
+    if (!aligned(x, 16) && M * v.cols != 0) return fail(MLXQ_ERR_INVALID_ARG, "X is not 16-byte aligned");
+    if ((rc = check_buf(y, M * v.rows, "Y"))) return rc;
+    if (overlap(y, M * v.rows * 2, x, M * v.cols * 2)) return fail(MLXQ_ERR_INVALID_ARG, "Y overlaps X");
+    if (overlaps_mx4(y, M * v.rows * 2, v)) return fail(MLXQ_ERR_INVALID_ARG, "output overlaps the weight buffers");
+    if (M == 0 || v.rows == 0) return ok();
+    return launch_status(launch_mx4_gemm(v, x, y, M, as_stream(stream)), "MX4 gemm launch");
+}
+
+// ---- mixture-of-experts layer -----------------------------------------------------------------
+size_t mlxq_moe_workspace_bytes(uint32_t hidden, uint32_t inter, uint32_t top_k, uint32_t m) {
+    (void)hidden;
+    return moe_workspace_bytes(inter, static_cast<int64_t>(m) * top_k);
+}
+
+int mlxq_moe(const void* router, const mlxq_weight* gate, const mlxq_weight* up, const mlxq_weight* down, uint32_t experts,
+             uint32_t top_k, uint32_t flags, const void* x, void* y, uint32_t m, void* workspace, size_t workspace_bytes,
+             uint64_t stream) {
+    WeightView g, u, d;
+    MoeCall c{};
+    int rc;
+    if ((rc = check_weight(gate, g)) || (rc = check_weight(up, u)) || (rc = check_weight(down, d))) return rc;
+    if ((rc = check_moe_shapes(g.N, g.K, u.N, u.K, d.N, d.K, experts, top_k, flags, m, 64, c))) return rc;
+    if ((rc = check_moe_weight(g, "gate")) || (rc = check_moe_weight(u, "up")) || (rc = check_moe_weight(d, "down"))) return rc;
+    if (g.gs != u.gs) return fail(MLXQ_ERR_GROUP_SIZE, "gate and up must have one group size");
+    if (m == 0) return ok();
+    auto hits = [&](const void* p, int64_t b) {
+        for (const WeightView* v : {&g, &u, &d})
+            if (overlap(p, b, v->packed, v->N * v->K) || overlap(p, b, v->scales, v->N * v->G * 2) ||
+                overlap(p, b, v->biases, v->N * v->G * 2))
+                return true;
+        return false;
+    };
+    if ((rc = check_moe_buffers(router, x, y, workspace, workspace_bytes, c, hits))) return rc;
+    return launch_status(launch_moe(c, g, u, d, as_stream(stream)), "expert layer launch");
+}
+
+int mlxq_mx4_moe(const void* router, const mlxq_mx4* gate, const mlxq_mx4* up, const mlxq_mx4* down, uint32_t experts,
+                 uint32_t top_k, uint32_t flags, const void* x, void* y, uint32_t m, void* workspace, size_t workspace_bytes,
+                 uint64_t stream) {
+    Mx4View g, u, d;
+    MoeCall c{};
+    int rc;
+    if ((rc = check_mx4(gate, g, "gate")) || (rc = check_mx4(up, u, "up")) || (rc = check_mx4(down, d, "down"))) return rc;
+    if ((rc = check_moe_shapes(g.rows, g.cols, u.rows, u.cols, d.rows, d.cols, experts, top_k, flags, m, 32, c))) return rc;
+    if (m == 0) return ok();
+    auto hits = [&](const void* p, int64_t b) { return overlaps_mx4(p, b, g) || overlaps_mx4(p, b, u) || overlaps_mx4(p, b, d); };
+    if ((rc = check_moe_buffers(router, x, y, workspace, workspace_bytes, c, hits))) return rc;
+    return launch_status(launch_mx4_moe(c, g, u, d, as_stream(stream)), "MX4 expert layer launch");
 }
 
 int mlxq_device_status(void) {

@@ -21,6 +21,13 @@ struct WeightView {
     uint32_t flags;          // MLXQ_WEIGHT_*
 };
 
+// An MX4 matrix: E2M1 codes and one E8M0 scale byte per 32 columns.
+struct Mx4View {
+    const uint8_t* codes;   // [rows, cols / 2] bytes
+    const uint8_t* scales;  // [rows, cols / 32]
+    int64_t rows, cols;
+};
+
 enum GemvMode { GEMV_PLAIN = 0, GEMV_SILU = 1, GEMV_SILU_RESID = 2 };
 
 // Device properties of the current device (cached per device).
@@ -141,5 +148,31 @@ cudaError_t reset_static_scratch_counters();
 size_t gemm_tc_scratch_bytes(const WeightView& w, int64_t m);
 cudaError_t launch_gemm_tc(const WeightView& w, const void* X, void* Y, int64_t m, cudaStream_t stream,
                            TcScratch scratch = TC_SCRATCH_POOL);
+
+// MX4: BF16 [rows, cols] -> codes and scales of `dst`, and back.
+cudaError_t launch_mx4_quantize(const void* x, const Mx4View& dst, cudaStream_t stream);
+cudaError_t launch_mx4_dequant(const Mx4View& w, void* out, cudaStream_t stream);
+// Y [m, rows] = X [m, cols] W^T, BF16 activations, 1 <= m <= kMx4GemmMaxM.
+constexpr int kMx4GemmMaxM = 64;
+cudaError_t launch_mx4_gemm(const Mx4View& w, const void* x, void* y, int64_t m, cudaStream_t stream);
+// Y [a.rows, w.rows] = A W^T, both operands in MX4.
+cudaError_t launch_mx4_matmul(const Mx4View& w, const Mx4View& a, void* y, cudaStream_t stream);
+
+// Mixture-of-experts layer for 1 <= m <= kMoeMaxTokens tokens.
+constexpr int kMoeMaxTokens = 64;
+constexpr int kMoeMaxExperts = 256;
+constexpr int kMoeMaxTopK = 16;
+struct MoeCall {
+    const void* router;
+    const void* x;
+    void* y;
+    void* workspace;
+    int experts, top_k, hidden, inter, m, softmax_all;
+};
+size_t moe_workspace_bytes(int64_t inter, int64_t slots);
+cudaError_t launch_moe(const MoeCall& c, const WeightView& gate, const WeightView& up, const WeightView& down,
+                       cudaStream_t stream);
+cudaError_t launch_mx4_moe(const MoeCall& c, const Mx4View& gate, const Mx4View& up, const Mx4View& down,
+                           cudaStream_t stream);
 
 }  // namespace mlxq
