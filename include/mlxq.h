@@ -274,6 +274,14 @@ MLXQ_API int mlxq_mx4_dequant(const mlxq_mx4* w, void* out, uint64_t stream);
 MLXQ_API int mlxq_mx4_gemm(const mlxq_mx4* w, const void* x, void* y, uint32_t m, uint64_t stream);
 
 /*
+ * mlxq_mx4_matmul.  Y = A W^T with both operands in MX4 (activations quantized
+ * with mlxq_mx4_quantize), any number of rows: the tensor cores take the codes
+ * and scales as they are, sums in fp32.  Y: BF16 [a.rows, w.rows].  w.cols ==
+ * a.cols; dimensions up to 2^30.
+ */
+MLXQ_API int mlxq_mx4_matmul(const mlxq_mx4* w, const mlxq_mx4* a, void* y, uint64_t stream);
+
+/*
  * A mixture-of-experts layer for 0 <= m <= 64 tokens:
  *   logits = x R^T;  S[t] = the top_k largest of token t (ties: lowest index);
  *   p = softmax over S[t], or over all experts with MLXQ_MOE_SOFTMAX_ALL;

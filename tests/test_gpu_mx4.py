@@ -219,3 +219,87 @@ def test_gemm_past_32_bits_of_codes():
     want = torch.zeros(N, dtype=torch.bfloat16, device="cuda")
     want[-1], want[N // 2] = K, 2 * K
     assert torch.equal(y[0], want)
+
+
+# (m, N, K): both operands in MX4; tiles are 256 x up to 224, k-blocks 256
+MATMUL = [(1, 1, 32), (16, 256, 256), (128, 256, 512), (224, 512, 1024), (5, 300, 96), (130, 260, 288), (300, 1000, 736),
+          (225, 257, 4128), (509, 1100, 544), (64, 4097, 1280), (2000, 3100, 256), (17, 5000, 2048)]
+
+
+@pytest.mark.parametrize("m,N,K", MATMUL)
+def test_matmul(m, N, K):
+    g, wc, ws, w = make(m + N, N, K)
+    ac, as_ = ref.random_weight(g, m, K, low=122, high=130)
+    a = mq.mx4_view(dev(ref.pack(ac)), dev(as_))
+    y = Guarded(m * N)
+    mq.mlxq_mx4_matmul(w, a, y.data_ptr())
+    torch.cuda.synchronize()
+    y.check_guards()
+    wv, av = ref.values(wc, ws), ref.values(ac, as_)
+    want = av @ wv.T
+    err = np.abs(bits_to_f64(y.value_bits()).reshape(m, N) - want)
+    assert np.all(err <= bound(np.abs(wv), np.abs(av), want, K)), float(err.max())
+
+
+def test_matmul_places_every_code_and_scale():
+    """One nonzero activation column at a time: Y is that weight column times a power of two, exactly."""
+    N, K, m = 300, 320, 320
+    g, wc, ws, w = make(3, N, K, low=110, high=140)
+    ac, as_ = np.zeros((m, K), np.uint8), np.full((m, K // 32), 127, np.uint8)
+    ac[np.arange(m), np.arange(K)] = 2 + 2 * (np.arange(K) % 3)  # 1, 2, 4
+    as_ += g.integers(0, 9, as_.shape).astype(np.uint8)
+    y = torch.empty(m, N, dtype=torch.bfloat16, device="cuda")
+    mq.mlxq_mx4_matmul(w, mq.mx4_view(dev(ref.pack(ac)), dev(as_)), y)
+    want = ref.values(ac, as_) @ ref.values(wc, ws).T
+    assert np.array_equal(bits_to_f64(host_bits(y)), want)
+
+
+def test_matmul_nan_scales_stay_in_their_rows():
+    N, K, m = 300, 288, 40
+    g, wc, ws, _ = make(4, N, K)
+    ac, as_ = ref.random_weight(g, m, K)
+    ws[270, 8], as_[33, 0] = 255, 255
+    y = torch.empty(m, N, dtype=torch.bfloat16, device="cuda")
+    mq.mlxq_mx4_matmul(mq.mx4_view(dev(ref.pack(wc)), dev(ws)), mq.mx4_view(dev(ref.pack(ac)), dev(as_)), y)
+    want = np.zeros((m, N), bool)
+    want[33, :], want[:, 270] = True, True
+    assert np.array_equal(np.isnan(bits_to_f64(host_bits(y))), want)
+
+
+def test_matmul_unaligned_scales_and_no_columns():
+    """Scale tables that are 4-byte but not 8-byte aligned; products of no columns are zero."""
+    N, K, m = 70, 512, 20
+    g, wc, ws, _ = make(8, N, K)
+    ac, as_ = ref.random_weight(g, m, K)
+    buf = torch.zeros(ws.size + 4, dtype=torch.uint8, device="cuda")
+    buf[4:] = dev(ws).reshape(-1)
+    codes = dev(ref.pack(wc))
+    y = torch.empty(m, N, dtype=torch.bfloat16, device="cuda")
+    mq.mlxq_mx4_matmul(mq.mx4_view(codes, buf[4:].view(N, -1)), mq.mx4_view(dev(ref.pack(ac)), dev(as_)), y)
+    wv, av = ref.values(wc, ws), ref.values(ac, as_)
+    assert np.all(np.abs(bits_to_f64(host_bits(y)) - av @ wv.T) <= bound(np.abs(wv), np.abs(av), av @ wv.T, K))
+    mq.mlxq_mx4_matmul(mq.mlxq_mx4(None, None, N, 0), mq.mlxq_mx4(None, None, m, 0), y)
+    assert not y.any()
+
+
+def test_quantize_then_matmul_in_a_graph():
+    """Prefill as a program makes it: activations quantised and multiplied, several times in a row."""
+    N, K, m = 500, 1056, 260
+    g = synth.rng(21)
+    wb, xb = synth.activations(g, N, K), synth.activations(g, m, K)
+    w, a, x = mq.mx4_empty(N, K), mq.mx4_empty(m, K), dev(xb)
+    mq.mlxq_mx4_quantize(dev(wb), w)
+    y = torch.zeros(m, N, dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        for _ in range(3):
+            mq.mlxq_mx4_quantize(x, a, s)
+            mq.mlxq_mx4_matmul(w, a, y, s)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    wv, av = ref.values(*ref.quantize(wb)), ref.values(*ref.quantize(xb))
+    want = av @ wv.T
+    assert np.all(np.abs(bits_to_f64(host_bits(y)) - want) <= bound(np.abs(wv), np.abs(av), want, K))

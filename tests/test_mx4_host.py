@@ -120,6 +120,22 @@ def test_gemm_checks_its_buffers():
     mq.mlxq_mx4_gemm(handle(), None, None, 0, 0)  # m == 0: nothing to do
 
 
+def test_matmul_checks_its_buffers():
+    bad = mq.MLXQ_ERR_INVALID_ARG
+    a = handle(rows=8, codes=16 * P, scales=17 * P)
+    c = lambda w, a, y: code_of(mq.mlxq_mx4_matmul, w, a, y, 0)
+    assert c(handle(), handle(cols=96, codes=16 * P, scales=17 * P), 8 * P) == mq.MLXQ_ERR_SHAPE
+    assert c(handle(cols=40), a, 8 * P) == mq.MLXQ_ERR_SHAPE
+    assert c(handle(), handle(codes=None), 8 * P) == bad
+    assert c(handle(codes=P + 4), a, 8 * P) == bad
+    assert c(handle(), a, None) == bad
+    assert c(handle(), a, 8 * P + 1) == bad
+    assert c(handle(), a, P + 16) == bad       # Y over the weight
+    assert c(handle(), a, 17 * P) == bad       # Y over the activations' scales
+    assert c(handle(rows=(1 << 30) + 1, cols=32, codes=1 << 40, scales=1 << 41), handle(8, 32), 8 * P) == mq.MLXQ_ERR_UNSUPPORTED
+    mq.mlxq_mx4_matmul(handle(), handle(rows=0), None, 0)
+
+
 def test_tensor_arguments_must_be_dense_and_typed():
     h = handle(4, 64)
     x = torch.zeros(4, 64, dtype=torch.bfloat16)

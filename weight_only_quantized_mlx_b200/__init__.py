@@ -49,7 +49,7 @@ MLXQ_DTYPE_F32 = 2
 EXPORTS = ("mlxq_load", "mlxq_dequant", "mlxq_gemv", "mlxq_gemv_silu_gate",
            "mlxq_gemv_silu_gate_resid", "mlxq_gemm", "mlxq_gemm_with", "mlxq_gemm_noalloc", "mlxq_release",
            "mlxq_last_error", "mlxq_device_status", "mlxq_dequant_as", "mlxq_quantize", "mlxq_selftest_wait_timeout",
-           "mlxq_selftest_fail_alloc", "mlxq_mx4_quantize", "mlxq_mx4_dequant", "mlxq_mx4_gemm",
+           "mlxq_selftest_fail_alloc", "mlxq_mx4_quantize", "mlxq_mx4_dequant", "mlxq_mx4_gemm", "mlxq_mx4_matmul",
            "mlxq_moe_workspace_bytes", "mlxq_moe", "mlxq_mx4_moe")
 
 
@@ -106,6 +106,7 @@ def lib() -> ctypes.CDLL:
             "mlxq_mx4_quantize": [vp, Q, u64],
             "mlxq_mx4_dequant": [Q, vp, u64],
             "mlxq_mx4_gemm": [Q, vp, vp, u32, u64],
+            "mlxq_mx4_matmul": [Q, Q, vp, u64],
             "mlxq_moe_workspace_bytes": [u32, u32, u32, u32],
             "mlxq_moe": [vp, W, W, W, u32, u32, u32, vp, vp, u32, vp, ctypes.c_size_t, u64],
             "mlxq_mx4_moe": [vp, Q, Q, Q, u32, u32, u32, vp, vp, u32, vp, ctypes.c_size_t, u64],
@@ -262,6 +263,11 @@ def mlxq_mx4_dequant(w: mlxq_mx4, out, stream=None) -> None:
 def mlxq_mx4_gemm(w: mlxq_mx4, x, y, m: int, stream=None) -> None:
     x, y = _dense(x, "bfloat16", "X", m * w.cols), _dense(y, "bfloat16", "Y", m * w.rows)
     _check(lib().mlxq_mx4_gemm(ctypes.byref(w), x, y, m, _stream(stream)))
+
+
+def mlxq_mx4_matmul(w: mlxq_mx4, a: mlxq_mx4, y, stream=None) -> None:
+    y = _dense(y, "bfloat16", "Y", a.rows * w.rows)
+    _check(lib().mlxq_mx4_matmul(ctypes.byref(w), ctypes.byref(a), y, _stream(stream)))
 
 
 def mlxq_moe_workspace_bytes(hidden: int, inter: int, top_k: int, m: int) -> int:

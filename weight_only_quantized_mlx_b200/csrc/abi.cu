@@ -811,6 +811,22 @@ int mlxq_mx4_gemm(const mlxq_mx4* w, const void* x, void* y, uint32_t m, uint64_
     return launch_status(launch_mx4_gemm(v, x, y, M, as_stream(stream)), "MX4 gemm launch");
 }
 
+int mlxq_mx4_matmul(const mlxq_mx4* w, const mlxq_mx4* a, void* y, uint64_t stream) {
+    Mx4View v, u;
+    int rc;
+    if ((rc = check_mx4(w, v, "w")) || (rc = check_mx4(a, u, "a"))) return rc;
+    if (v.cols != u.cols)
+        return fail(MLXQ_ERR_SHAPE, "w has %u columns and a has %u", w->cols, a->cols);
+    if (v.rows > kMaxDim || u.rows > kMaxDim || v.cols > kMaxDim)
+        return fail(MLXQ_ERR_UNSUPPORTED, "MX4 matmul: a dimension is beyond 2^30");
+    if (v.rows != 0 && u.rows > (int64_t{1} << 50) / v.rows) return fail(MLXQ_ERR_SHAPE, "Y is beyond any device");
+    const int64_t yb = u.rows * v.rows * 2;
+    if ((rc = check_buf(y, u.rows * v.rows, "Y"))) return rc;
+    if (overlaps_mx4(y, yb, v) || overlaps_mx4(y, yb, u)) return fail(MLXQ_ERR_INVALID_ARG, "Y overlaps an operand");
+    if (yb == 0) return ok();
+    return launch_status(launch_mx4_matmul(v, u, y, as_stream(stream)), "MX4 matmul launch");
+}
+
 // ---- mixture-of-experts layer -----------------------------------------------------------------
 size_t mlxq_moe_workspace_bytes(uint32_t hidden, uint32_t inter, uint32_t top_k, uint32_t m) {
     (void)hidden;

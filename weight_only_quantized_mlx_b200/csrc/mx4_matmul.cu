@@ -1,0 +1,366 @@
+// Y = A W^T with both operands in MX4, on the block-scaled tensor instruction
+// (tcgen05.mma kind::mxf4): E2M1 codes straight from memory, one E8M0 scale per
+// 32 columns applied inside the tensor core, fp32 sums in TMEM.
+//
+//   tile: 256 weight rows (two MMA M = 128 halves) x BN activation rows (MMA N,
+//         up to 224), over all of K in k-blocks of 256 columns (one 128-byte row
+//         of codes, four MMAs of K = 64 per half)
+//   warp 0      TMA: the codes of both operands (128-byte swizzle)
+//   warp 1      allocates TMEM; one lane copies each k-block's scales into TMEM
+//               (tcgen05.cp) and issues the MMAs
+//   warps 2, 3  scales of the weight rows and of the activation rows: 8 bytes a
+//               row and k-block, put into the 128 x 4 order that tcgen05.cp and
+//               the MMA expect (row r, group g of a set of four: byte
+//               (r % 32) 16 + (r / 32) 4 + g)
+//   warps 4-11  read the accumulators (tcgen05.ld) as BF16 into registers,
+//               hand TMEM back and store Y while the next tile's MMAs run
+//
+// TMEM (512 columns): 2 x 224 columns of sums, 2 x 32 columns of scales (a
+// k-block's: two halves and two sets of four columns for the weight, two sets of
+// eight for the activations).  Why 256 x 224: at the 4-bit rate a k-block of
+// codes must arrive in about half a microsecond, so the bytes from L2 per
+// multiply bound the kernel, and this is the squarest tile that leaves TMEM
+// room for scales.  Columns behind K and rows behind the operands read as zero
+// codes under scale 1.
+//
+// All waits are bounded; after one gives up the producers and the MMA thread
+// issue nothing more and wait (bounded) for what they issued.
+#include "device_common.cuh"
+#include "kernels.h"
+#include "mx4_common.cuh"
+#include "tensor_map.h"
+
+namespace mlxq {
+namespace {
+
+constexpr int kBM = 256;                     // weight rows per tile
+constexpr int kMaxBN = 224;                  // activation rows per tile
+constexpr int kBK = 256;                     // columns per k-block
+constexpr int kStages = 3;
+constexpr uint32_t kStageW = kBM * 128;      // codes of the weight rows
+constexpr uint32_t kStageX = kMaxBN * 128;   // codes of the activation rows
+constexpr uint32_t kStageS = 2048;           // scales of one operand: [half][set][32][16]
+constexpr uint32_t kStageBytes = kStageW + kStageX + 2 * kStageS;
+constexpr int kFirstEpilogue = 4;
+constexpr int kThreads = (kFirstEpilogue + 8) * 32;
+constexpr uint32_t kAccCols = kMaxBN;        // TMEM columns of one half's sums
+constexpr uint32_t kScaleCol = 2 * kAccCols; // then two buffers of 32 columns of scales
+static_assert(kScaleCol + 2 * 32 <= 512, "TMEM columns");
+
+struct MatmulParams {
+    uint16_t* Y;
+    const uint8_t* w_scales;
+    const uint8_t* a_scales;
+    int N, m, G;        // weight rows, activation rows, scale bytes per row
+    int BN, num_kb;
+    int scale_load;     // bytes per load of scales: 8, 4 or 1
+    uint32_t idesc;
+    unsigned int* status;
+};
+
+__device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// 32 rows x 16 bytes of shared memory -> four TMEM columns, in all four lane quadrants
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// K-major operand, rows of 128 bytes, 128-byte swizzle, 8-row groups 1024 bytes apart
+__device__ __forceinline__ uint64_t codes_desc(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(1u) << 16 |
+           static_cast<uint64_t>(1024u >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(2u) << 61;
+}
+// 32 rows of 16 bytes, no swizzle, 8-row groups 128 bytes apart
+__device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(1u) << 16 |
+           static_cast<uint64_t>(128u >> 4) << 32 | static_cast<uint64_t>(1u) << 46;
+}
+
+// The eight scale bytes of one row and k-block; 127 (scale 1) where there is none.
+__device__ __forceinline__ uint2 load_scales(const uint8_t* row, bool live, int g0, int G, int bytes) {
+    uint2 v = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    if (!live) return v;
+    if (bytes == 8) return __ldg(reinterpret_cast<const uint2*>(row + g0));
+    if (bytes == 4) {
+        v.x = __ldg(reinterpret_cast<const uint32_t*>(row + g0));
+        if (g0 + 4 < G) v.y = __ldg(reinterpret_cast<const uint32_t*>(row + g0 + 4));
+        return v;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (g0 + i < G) v.x = (v.x & ~(0xFFu << (8 * i))) | static_cast<uint32_t>(__ldg(row + g0 + i)) << (8 * i);
+        if (g0 + 4 + i < G) v.y = (v.y & ~(0xFFu << (8 * i))) | static_cast<uint32_t>(__ldg(row + g0 + 4 + i)) << (8 * i);
+    }
+    return v;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    k_mx4_matmul(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const MatmulParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[3 * kStages + 3];
+    __shared__ uint32_t tmem_slot;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;  // swizzle atoms
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tiles_n = (p.N + kBM - 1) / kBM, tiles = tiles_n * ((p.m + p.BN - 1) / p.BN);
+    const int num_kb = p.num_kb;
+
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(s); };                 // codes landed
+    auto sfull = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(kStages + s); };      // scales written
+    auto empty = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(2 * kStages + s); };  // stage read
+    const uint32_t acc_full = bar0 + 8u * 3 * kStages, acc_empty = acc_full + 8u, drain = acc_full + 16u;
+    auto W_of = [&](int s) { return base + static_cast<uint32_t>(s) * kStageBytes; };
+    auto X_of = [&](int s) { return W_of(s) + kStageW; };
+    auto SW_of = [&](int s) { return X_of(s) + kStageX; };
+    auto SX_of = [&](int s) { return SW_of(s) + kStageS; };
+
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(sfull(s), 2);
+            mbar_init(empty(s), 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 8);
+        mbar_init(drain, 1);
+        mbar_fence_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = tmem_slot;
+    pdl_wait();
+
+    if (warp == 0) {
+        // ---------------- codes ----------------
+        if (lane == 0) {
+            prefetch_tmap(&tm_w);
+            prefetch_tmap(&tm_a);
+            const uint64_t pol = policy_evict_last();  // every tile of codes serves many tiles of Y
+            const uint32_t bytes = kStageW + static_cast<uint32_t>(p.BN) * 128u;
+            bool ok = true;
+            int it = 0;
+            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+                const int n0 = (tile % tiles_n) * kBM, m0 = (tile / tiles_n) * p.BN;
+                for (int kb = 0; kb < num_kb; ++kb, ++it) {
+                    const int s = it % kStages;
+                    if (it >= kStages) ok = mbar_wait(empty(s), ((it / kStages) - 1) & 1, p.status);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(full(s), bytes);
+                    tma_load_2d(W_of(s), &tm_w, kb * 128, n0, full(s), pol);
+                    tma_load_2d(X_of(s), &tm_a, kb * 128, m0, full(s), pol);
+                }
+            }
+            // every issued copy has landed before the block may exit
+            for (int u = it > kStages ? it - kStages : 0; u < it; ++u)
+                if (!mbar_wait(full(u % kStages), (u / kStages) & 1, p.status)) break;
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA ----------------
+        if (lane == 0) {
+            bool ok = true;
+            int it = 0, t = 0;
+            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++t) {
+                if (t >= 1) ok = mbar_wait(acc_empty, (t - 1) & 1, p.status);
+                if (!ok) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                for (int kb = 0; kb < num_kb; ++kb, ++it) {
+                    const int s = it % kStages;
+                    ok = mbar_wait(full(s), (it / kStages) & 1, p.status) && mbar_wait(sfull(s), (it / kStages) & 1, p.status);
+                    if (!ok) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    // scales of the k-block: weight half h, set q at sc + 8h + 4q; activations set q at sc + 16 + 8q
+                    const uint32_t sc = tmem + kScaleCol + 32u * (it & 1);
+                    const uint64_t sw = scales_desc(SW_of(s)), sx = scales_desc(SX_of(s));
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        copy_scales(sc + 4u * q, sw + 32u * q);                 // 512 bytes apart
+                        copy_scales(sc + 8u + 4u * q, sw + 64u + 32u * q);      // half 1, 1024 bytes on
+                        copy_scales(sc + 16u + 8u * q, sx + 32u * q);
+                        if (p.BN > 128) copy_scales(sc + 20u + 8u * q, sx + 64u + 32u * q);
+                    }
+                    const uint64_t a0 = codes_desc(W_of(s)), a1 = codes_desc(W_of(s) + 128u * 128u), b = codes_desc(X_of(s));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t acc = (kb != 0 || kk != 0) ? 1u : 0u;
+                        // the two scales of this K = 64 are bytes 0, 1 or 2, 3 of a column
+                        const uint32_t id = p.idesc | static_cast<uint32_t>(2 * (kk & 1)) << 4 | static_cast<uint32_t>(2 * (kk & 1)) << 29;
+                        const uint32_t q = static_cast<uint32_t>(kk >> 1);
+                        umma_mxf4(tmem, a0 + 2u * kk, b + 2u * kk, id, sc + 4u * q, sc + 16u + 8u * q, acc);
+                        umma_mxf4(tmem + kAccCols, a1 + 2u * kk, b + 2u * kk, id, sc + 8u + 4u * q, sc + 16u + 8u * q, acc);
+                    }
+                    commit(empty(s));
+                }
+                if (ok) commit(acc_full);
+            }
+            // everything this thread issued has finished before TMEM is freed
+            commit(drain);
+            mbar_wait(drain, 0, p.status);
+        }
+        __syncwarp();
+    } else if (warp < kFirstEpilogue) {
+        // ---------------- scales ----------------
+        const bool weight = warp == 2;
+        const uint8_t* scales = weight ? p.w_scales : p.a_scales;
+        const int rows = weight ? p.N : p.m, span = weight ? kBM : p.BN;
+        uint2 v[8];
+        auto load = [&](int tile, int kb) {
+            const int r0 = weight ? (tile % tiles_n) * kBM : (tile / tiles_n) * p.BN;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = lane + 32 * i;
+                v[i] = load_scales(scales + static_cast<int64_t>(r0 + r) * p.G, r < span && r0 + r < rows, kb * 8, p.G, p.scale_load);
+            }
+        };
+        bool ok = true;
+        int it = 0;
+        if (static_cast<int>(blockIdx.x) < tiles) load(blockIdx.x, 0);
+        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            for (int kb = 0; kb < num_kb; ++kb, ++it) {
+                const int s = it % kStages;
+                uint2 c[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) c[i] = v[i];
+                // the next k-block's loads are in flight while this one waits for its stage
+                if (kb + 1 < num_kb) load(tile, kb + 1);
+                else if (tile + static_cast<int>(gridDim.x) < tiles) load(tile + gridDim.x, 0);
+                if (it >= kStages) ok = mbar_wait(empty(s), ((it / kStages) - 1) & 1, p.status);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = (weight ? SW_of(s) : SX_of(s)) + static_cast<uint32_t>(lane) * 16u;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 1024u * h), "r"(c[4 * h].x), "r"(c[4 * h + 1].x),
+                                 "r"(c[4 * h + 2].x), "r"(c[4 * h + 3].x)
+                                 : "memory");
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 1024u * h + 512u), "r"(c[4 * h].y),
+                                 "r"(c[4 * h + 1].y), "r"(c[4 * h + 2].y), "r"(c[4 * h + 3].y)
+                                 : "memory");
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sfull(s));
+            }
+        }
+    } else {
+        // ---------------- epilogue ----------------
+        const int e = warp - kFirstEpilogue, half = e >> 2, quad = warp & 3;  // TMEM lanes 32 quad ..
+        const int64_t N = p.N;
+        int t = 0;
+        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++t) {
+            const int n = (tile % tiles_n) * kBM + half * 128 + quad * 32 + lane, m0 = (tile / tiles_n) * p.BN;
+            const bool ok = mbar_wait(acc_full, t & 1, p.status);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(half) * kAccCols;
+            uint32_t y[kMaxBN / 2];  // BF16 pairs: columns 2i, 2i + 1
+#pragma unroll
+            for (int c = 0; c < kMaxBN / 16; ++c) {
+                if (c * 16 < p.BN) {
+                    uint32_t r[16];
+                    tmem_ld16(src + 16u * c, r);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[c * 8 + i] = pack_bf16x2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+                }
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty);
+            if (n < p.N) {
+                uint16_t* out = p.Y + static_cast<int64_t>(m0) * N + n;
+                const int rows = min(p.BN, p.m - m0);
+#pragma unroll
+                for (int i = 0; i < kMaxBN / 2; ++i) {
+                    if (2 * i < rows) out[0] = static_cast<uint16_t>(y[i]);
+                    if (2 * i + 1 < rows) out[N] = static_cast<uint16_t>(y[i] >> 16);
+                    out += 2 * N;
+                }
+            }
+        }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+// Activation rows per tile: the multiple of 16 that ends first, counting a
+// k-block as its bytes (256 + BN rows of codes: they bound the kernel).
+int pick_bn(int64_t m, int64_t N, int sms) {
+    int best = 16;
+    int64_t best_cost = INT64_MAX;
+    for (int bn = 16; bn <= kMaxBN; bn += 16) {
+        const int64_t tiles = ((N + kBM - 1) / kBM) * ((m + bn - 1) / bn);
+        const int64_t cost = ((tiles + sms - 1) / sms) * (kBM + bn);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = bn;
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_matmul(const Mx4View& w, const Mx4View& a, void* y, cudaStream_t stream) {
+    if (w.cols == 0) return cudaMemsetAsync(y, 0, static_cast<size_t>(a.rows * w.rows * 2), stream);  // empty sums
+    static std::atomic<int> configured[64];
+    const size_t smem = kStages * kStageBytes + 1024;
+    cudaError_t e = ensure_dynamic_smem(k_mx4_matmul, smem, configured);
+    if (e != cudaSuccess) return e;
+    const int sms = device_info().sm_count;
+    MatmulParams p{};
+    p.Y = static_cast<uint16_t*>(y);
+    p.w_scales = w.scales;
+    p.a_scales = a.scales;
+    p.N = static_cast<int>(w.rows);
+    p.m = static_cast<int>(a.rows);
+    p.G = static_cast<int>(w.cols / kMxBlock);
+    p.BN = pick_bn(a.rows, w.rows, sms);
+    p.num_kb = static_cast<int>((w.cols + kBK - 1) / kBK);
+    const bool a8 = ((reinterpret_cast<uintptr_t>(w.scales) | reinterpret_cast<uintptr_t>(a.scales)) & 7u) == 0;
+    p.scale_load = p.G % 8 == 0 && a8 ? 8 : (p.G % 4 == 0 ? 4 : 1);
+    // kind::mxf4: A and B E2M1 (1), scales UE8M0 (bit 23), N / 8, M / 128
+    p.idesc = 1u << 7 | 1u << 10 | static_cast<uint32_t>(p.BN / 8) << 17 | 1u << 23 | 1u << 27;
+    p.status = device_status_ptr();
+    CUtensorMap tm_w, tm_a;
+    if (!encode_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, static_cast<uint64_t>(w.cols / 2), static_cast<uint64_t>(w.rows),
+                   static_cast<uint64_t>(w.cols / 2), 128, kBM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, static_cast<uint64_t>(a.cols / 2), static_cast<uint64_t>(a.rows),
+                   static_cast<uint64_t>(a.cols / 2), 128, static_cast<uint32_t>(p.BN), CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    const int64_t tiles = ((w.rows + kBM - 1) / kBM) * ((a.rows + p.BN - 1) / p.BN);
+    if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;
+    return launch_pdl(k_mx4_matmul, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kThreads), smem, stream, tm_w, tm_a, p);
+}
+
+}  // namespace mlxq
