@@ -9,7 +9,7 @@
 //
 // k_moe_experts: one persistent block per SM (cooperative launch).  Each block
 // builds the lists of tokens per expert, then streams its share of the hit
-// experts' gate and up rows (stream_tile.cuh; the 16 rows of a tile are 8 gate
+// experts' gate and up rows (row_stream.cuh; the 16 rows of a tile are 8 gate
 // rows and the same 8 up rows, so silu(gate) * up is a lane's own business),
 // writes h, crosses a grid barrier, and streams its share of the down rows over
 // all experts at once.  HBM-bound on the experts hit; each weight byte is read
@@ -22,7 +22,7 @@
 
 #include <utility>
 
-#include "stream_tile.cuh"
+#include "row_stream.cuh"
 
 namespace mlxq {
 namespace {
@@ -178,6 +178,18 @@ struct ExpertParams {
     unsigned int* status;
 };
 
+// Which activation rows an expert's MMA columns hold.  A slot is token * top_k
+// + choice.  Up to 8 tokens (NT == 1): column = token, eight entries per expert,
+// -1 where the token did not choose it.  Otherwise the expert's slots one after
+// another, padded with -1 to a multiple of 8.
+struct Columns {
+    const int16_t* cols;
+    const int16_t* off;  // first entry of active expert a
+    const int16_t* cnt;
+    int top_k;
+    __device__ __forceinline__ int slot(int a, int c) const { return cols[off[a] + c]; }
+};
+
 constexpr int kMaxSlots = kMoeMaxTokens * kMoeMaxTopK;
 constexpr int kMaxCols = kMaxSlots + 7 * kMaxExperts;  // lists padded to multiples of 8
 
@@ -262,121 +274,307 @@ __device__ __forceinline__ bool grid_barrier(unsigned int* count, unsigned int* 
     return *stop == 0;
 }
 
-template <class F, int NT>
-__global__ void __launch_bounds__(kStreamThreads, 1) k_moe_experts(const __grid_constant__ ExpertParams<F> p) {
-    extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t* areas = smem + kStreamWarps * kRingBytes;
-    ExpertLists& L = *reinterpret_cast<ExpertLists*>(areas + kStreamWarps * kAreaBytes);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
-    pdl_wait();
-    build_lists<NT>(L, p.ws.ids, p.m * p.top_k, p.top_k, p.E);
-    const Columns cm{L.cols, L.off, L.cnt, p.top_k};
-    const int A = L.experts;
+// ---- the streaming phases --------------------------------------------------------------------
+// Shared memory: rings | lists | gate and up: areas, column exponents, activations
+//                              | down: areas.
+template <int NT>
+struct Smem {
+    static constexpr uint32_t kDownArea = NT == 1 ? 2048 : 16 * (8 * NT + 4) * 4;  // a warp's sums of the down phase
+    static constexpr uint32_t kLists = kStreamWarps * kRingBytes;
+    static constexpr uint32_t kAreas = (kLists + sizeof(ExpertLists) + 127) / 128 * 128;
+    static constexpr uint32_t kFields = kAreas + kStreamWarps * kSharedArea;
+    static constexpr uint32_t kX = kFields + 2 * kMoeMaxTokens * 4;
+    static constexpr uint32_t kTotal = 227 * 1024;
+    static constexpr uint32_t kXBytes = kTotal - kX;
+    static_assert(kX % 16 == 0 && kX + 16 * 1024 <= kTotal, "room for one step of 64 columns");
+    static_assert(kAreas + kStreamWarps * kDownArea <= kTotal && kDownArea % 16 == 0, "areas of the down phase");
+};
 
-    // ---- gate and up: flattened rows [lo, hi) of A x I, in octets (I % 8 == 0) ----
-    {
-        const int64_t rows = static_cast<int64_t>(A) * p.I;
-        const int64_t lo = rows * blockIdx.x / gridDim.x, hi = rows * (blockIdx.x + 1) / gridDim.x;
-        const int64_t o0 = lo >> 3;
-        const int octets = hi > lo ? static_cast<int>(((hi - 1) >> 3) - o0) + 1 : 0;
-        const int per = p.I >> 3;  // octets of an expert
-        const Share sh(octets, (p.H + F::kStepCols - 1) / F::kStepCols, 1, warp);
-        float4* area = reinterpret_cast<float4*>(areas + warp * kAreaBytes);
-        const float4* group_area = reinterpret_cast<const float4*>(areas + sh.group * sh.k_warps * kAreaBytes);
-        constexpr int kAreaVecs = kAreaBytes / 16;
-        constexpr int kBatch = 8 / NT;  // tiles between two joins
-        Cursor pc(sh);
-        uint32_t pslot = 0, cslot = 0;
-        auto issue = [&]() {
-            if (pc.tile < sh.tiles) {
-                const int64_t o = o0 + pc.tile;
-                const int a = static_cast<int>(o / per);
-                const int64_t row = static_cast<int64_t>(L.act[a]) * p.I + (o - static_cast<int64_t>(a) * per) * 8 + g;
-                const bool live = 8 * o + g >= lo && 8 * o + g < hi;
-                const StepRows r{row, row, live, live};
-                F::issue(p.gate, p.up, ring + pslot * kStageBytes, lane, r, pc.step);
-                pc.next(sh);
+// gate and up, then h = p silu(gate) up, for the flattened rows [lo, hi) of
+// (hit experts) x I, in octets (I % 8 == 0): a tile is 8 gate rows and the
+// same 8 up rows, so the lane that holds a gate sum holds its up sum.  With up
+// to 8 tokens all tiles are one segment (column = token), else a segment is an
+// expert (columns = its tokens).
+template <class F, int NT>
+struct GateUpJob {
+    const ExpertParams<F>& p;
+    const typename F::Mat& mat;
+    const ExpertLists& L;
+    Columns cm;
+    int64_t lo, hi;
+    int K, per, o0, octets, a_first, segs;  // per: octets of an expert; o0: the first octet (A I / 8 < 2^26)
+
+    __device__ __forceinline__ GateUpJob(const ExpertParams<F>& p_, const ExpertLists& L_, const Columns& cm_)
+        : p(p_), mat(p_.gate), L(L_), cm(cm_) {
+        const int64_t rows = static_cast<int64_t>(L.experts) * p.I;
+        lo = rows * blockIdx.x / gridDim.x;
+        hi = rows * (blockIdx.x + 1) / gridDim.x;
+        K = p.H;
+        per = p.I >> 3;
+        o0 = static_cast<int>(lo >> 3);
+        octets = lo < hi ? static_cast<int>((hi - 1) >> 3) - o0 + 1 : 0;
+        a_first = o0 / per;
+        segs = octets == 0 ? 0 : (NT == 1 ? 1 : (o0 + octets - 1) / per - a_first + 1);
+    }
+    __device__ __forceinline__ int begin(int s) const { return NT == 1 ? 0 : max((a_first + s) * per - o0, 0); }
+    __device__ __forceinline__ int end(int s) const { return NT == 1 ? octets : min((a_first + s + 1) * per - o0, octets); }
+    __device__ __forceinline__ int cols(int s) const { return NT == 1 ? p.m : static_cast<int>(L.cnt[a_first + s]); }
+    __device__ __forceinline__ const uint16_t* x_row(int s, int c) const {
+        const int token = NT == 1 ? c : cm.slot(a_first + s, c) / p.top_k;
+        return p.x + static_cast<int64_t>(token) * p.H;
+    }
+    __device__ __forceinline__ typename F::Feed feed(int tile, int lane) const {
+        const int o = o0 + tile, a = o / per, g = lane >> 2;
+        const int64_t row = static_cast<int64_t>(L.act[a]) * p.I + (o - a * per) * 8 + g;
+        const int64_t flat = 8 * static_cast<int64_t>(o) + g;
+        const bool live = flat >= lo && flat < hi;
+        return F::feed(p.gate, p.up, row, row, live, live, lane);
+    }
+    __device__ __forceinline__ uint32_t key(int tile, int lane) const {
+        const int o = o0 + tile, a = o / per;
+        return F::row_key(p.gate, static_cast<uint32_t>(L.act[a]) * static_cast<uint32_t>(p.I) +
+                                      static_cast<uint32_t>((o - a * per) * 8 + (lane >> 2)));
+    }
+    __device__ __forceinline__ void store(int s, int tile, int n, int lane, const float4& v) const {
+        const int o = o0 + tile, a = o / per, g = lane >> 2;
+        const int64_t flat = 8 * static_cast<int64_t>(o) + g;
+        if (flat < lo || flat >= hi) return;
+        const int row = (o - a * per) * 8 + g;
+        const float gate[2] = {v.x, v.y}, up[2] = {v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int c = n * 8 + 2 * (lane & 3) + i;
+            const int slot = c < cols(s) ? cm.slot(a, c) : -1;
+            if (slot < 0) continue;
+            const float h = p.ws.share[slot] * (__fdiv_rn(gate[i], 1.0f + expf(-gate[i])) * up[i]);
+            p.ws.h[static_cast<int64_t>(slot) * p.I + F::place(row)] = static_cast<uint16_t>(pack_bf16x2(h, 0.f));
+        }
+    }
+};
+
+// y[token][row] = sum over hit experts a and columns k of Wd_a[row, k] h[slot][k]
+// for the block's rows [lo, hi).  Tiles are 16 rows; every expert's slice of a
+// tile goes into one accumulator, so the sum over experts needs no second pass
+// and no atomics: with up to 8 tokens column = token and the fragment itself
+// accumulates, else each warp adds an expert's columns to its own
+// [16][tokens] sums in shared memory.  The warps that share a tile join in warp
+// order, so results do not depend on timing.  h is read once or twice per
+// block, so it is not staged: a lane loads the next step's first column tile
+// before it multiplies the present one.  `ready` runs once the ring has been
+// filled (weights only) and before h is read; false ends the phase.
+template <class F, int NT, class Params, class Ready>
+__device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L, const Columns& cm, uint32_t ring,
+                                           uint8_t* areas, Ready ready) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int lo = static_cast<int>(static_cast<int64_t>(p.H) * blockIdx.x / gridDim.x);
+    const int hi = static_cast<int>(static_cast<int64_t>(p.H) * (blockIdx.x + 1) / gridDim.x);
+    const int tiles = (hi - lo + 15) / 16, S = (p.I + F::kStepCols - 1) / F::kStepCols, A = L.experts, all = A * S;
+    int wk = 1, best = 0x7FFFFFFF;
+    for (int k = 1; k <= kStreamWarps; k *= 2) {
+        const int groups = kStreamWarps / k, cost = (tiles + groups - 1) / groups * ((all + k - 1) / k + (k > 1 ? 2 : 0));
+        if (cost < best) {
+            best = cost;
+            wk = k;
+        }
+    }
+    const int groups = kStreamWarps / wk, group = warp / wk, kw = warp - group * wk;
+    // This warp's steps of every tile: a contiguous range of all experts' steps,
+    // so that it changes expert (new rows of h, sums to put away) as seldom as can be.
+    const int first = static_cast<int>(static_cast<int64_t>(all) * kw / wk);
+    const int own = static_cast<int>(static_cast<int64_t>(all) * (kw + 1) / wk) - first;
+    const int a0 = first / S, s0 = first % S;
+    int left = own;  // steps of ptile still to be issued
+    constexpr int kBatch = NT == 1 ? 4 : 1;           // tiles between two joins
+    constexpr int kAreaFloats = Smem<NT>::kDownArea / 4;
+    constexpr int kStride = NT * 8 + 1;               // NT > 1: floats per row of the area
+    float* area = reinterpret_cast<float*>(areas + warp * Smem<NT>::kDownArea);
+    const float* group_area = reinterpret_cast<const float*>(areas + group * wk * Smem<NT>::kDownArea);
+
+    int ptile = own ? group : tiles, pa = a0, pstep = s0;
+    uint32_t pslot = 0, cslot = 0;
+    typename F::Feed feed;
+    auto refeed = [&]() {
+        if (ptile >= tiles) return;
+        const int r = lo + ptile * 16 + g;
+        const int64_t row = static_cast<int64_t>(L.act[pa]) * p.H + r;
+        feed = F::feed(p.down, p.down, row, row + 8, r < hi, r + 8 < hi, lane);
+    };
+    refeed();
+    auto issue = [&]() {
+        if (ptile < tiles) {
+            F::issue(p.down, feed, ring + pslot * kStageBytes, lane, pstep);
+            ++pstep;
+            if (--left == 0) {
+                left = own;
+                pa = a0;
+                pstep = s0;
+                ptile += groups;
+                refeed();
+            } else if (pstep == S) {
+                pstep = 0;
+                ++pa;
+                refeed();
             }
-            cp_async_commit();
-            pslot = (pslot + 1) % kDepth;
-        };
+        }
+        cp_async_commit();
+        pslot = pslot + 1 == kDepth ? 0 : pslot + 1;
+    };
 #pragma unroll 1
-        for (int i = 0; i < kDepth - 1; ++i) issue();
-        const int own = sh.own_steps();
-        for (int tile0 = sh.group; tile0 < sh.tiles; tile0 += sh.groups * kBatch) {
-            int batch = 0;
-            for (; batch < kBatch; ++batch) {
-                const int tile = tile0 + batch * sh.groups;
-                if (tile >= sh.tiles) break;
-                const int64_t o = o0 + tile;
-                const int a = static_cast<int>(o / per);
-                const uint32_t low = static_cast<uint32_t>(L.act[a]) * static_cast<uint32_t>(p.I) +
-                                     static_cast<uint32_t>((o - static_cast<int64_t>(a) * per) * 8 + g);
-                const int nt = NT == 1 ? 1 : (L.cnt[a] + 7) / 8;
-                float acc[NT][4];
-                const uint16_t* xp[NT];
+    for (int i = 0; i < kDepth - 1; ++i) issue();
+    if (!ready()) {
+        cp_async_wait<0>();
+        return;
+    }
+
+    for (int tile0 = group; tile0 < tiles; tile0 += groups * kBatch) {
+        int batch = 0;
+        for (; batch < kBatch; ++batch) {
+            const int tile = tile0 + batch * groups;
+            if (tile >= tiles) break;
+            float acc[NT][4];
+            const uint16_t* xp[NT];  // this lane's rows of h, at its place in a step
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+                xp[n] = nullptr;
+            }
+            if (NT > 1) {
+                for (int i = lane; i < 16 * kStride; i += 32) area[i] = 0.f;
+                __syncwarp();
+            }
+            auto scatter = [&](int a, int nt) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
+                    if (n >= nt) break;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int s = cm.slot(a, n * 8 + 2 * t + i);
+                        if (s >= 0) {
+                            const int token = s / cm.top_k;
+                            area[g * kStride + token] += acc[n][i];
+                            area[(g + 8) * kStride + token] += acc[n][2 + i];
+                        }
+                    }
                     acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-                    const int s = n < nt ? cm.slot(a, n * 8 + g) : -1;
-                    xp[n] = s >= 0 ? p.x + static_cast<int64_t>(s / p.top_k) * p.H : nullptr;
                 }
-                int step = sh.kw;
-                for (int it = 0; it < own; ++it) {
-                    cp_async_wait<kDepth - 2>();
-                    __syncwarp();  // the quad's scales have landed; the slot refilled below is read out
-                    issue();
-                    F::template consume<NT>(p.gate, ring + cslot * kStageBytes, lane, low, step, xp, nt, acc);
-                    cslot = (cslot + 1) % kDepth;
-                    step += sh.k_warps;
+                __syncwarp();
+            };
+            auto column = [&](int a, int n) -> const uint16_t* {
+                const int s = cm.slot(a, n * 8 + g);
+                return s >= 0 ? p.ws.h + static_cast<int64_t>(s) * p.I + t * (8 * F::kPieces) : nullptr;
+            };
+            auto fetch = [&](uint4 (&v)[F::kPieces], const uint16_t* row, int step) {
+                const int k = step * F::kStepCols;
+                const bool in = row != nullptr && k + t * (8 * F::kPieces) < p.I;
+#pragma unroll
+                for (int i = 0; i < F::kPieces; ++i) {
+                    v[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (in) v[i] = ldg128(row + k + 8 * i);
                 }
+            };
+            int a = a0, step = s0, nt = NT == 1 || own == 0 ? 1 : (cm.cnt[a] + 7) / 8;
+            uint4 x0[F::kPieces];
+            if (own) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                    if (n < nt) area[(batch * NT + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+                    if (n < nt) xp[n] = column(a, n);
+                fetch(x0, xp[0], step);
             }
-            group_sync(sh.group, sh.k_warps);
-            for (int i = sh.kw * 32 + lane; i < batch * NT * 32; i += sh.k_warps * 32) {
-                const int b = i / (NT * 32), n = (i >> 5) % NT, l = i & 31;
-                const int64_t o = o0 + tile0 + b * sh.groups;
-                const int a = static_cast<int>(o / per);
-                if (NT > 1 && n >= (L.cnt[a] + 7) / 8) continue;
+            for (int it = 0; it < own; ++it) {
+                // the step after this one
+                int na = a, nstep = step + 1;
+                if (nstep == S) {
+                    nstep = 0;
+                    ++na;
+                }
+                const bool more = it + 1 < own, turn = more && na != a;
+                const uint16_t* nx = xp[0];
+                if (turn) nx = column(na, 0);
+                uint4 x1[F::kPieces];
+                if (more) fetch(x1, nx, nstep);
+                const uint32_t key = F::row_key(p.down, static_cast<uint32_t>(L.act[a]) * static_cast<uint32_t>(p.H) +
+                                                            static_cast<uint32_t>(lo + tile * 16 + g));
+                cp_async_wait<kDepth - 2>();
+                __syncwarp();  // the quad's scales have landed; the slot refilled below is read out
+                issue();
+                const int k = step * F::kStepCols;
+                const bool in = k + t * (8 * F::kPieces) < p.I;
+                F::template consume<NT>(p.down, ring + cslot * kStageBytes, lane, key, step, nt, acc, [&](int i, int n) {
+                    if (n == 0) return x0[i];
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (xp[n] != nullptr && in) v = ldg128(xp[n] + k + 8 * i);
+                    return v;
+                });
+                cslot = cslot + 1 == kDepth ? 0 : cslot + 1;
+                if (turn || !more) {
+                    if (NT > 1) scatter(a, nt);
+                    if (turn) {
+                        nt = NT == 1 ? 1 : (cm.cnt[na] + 7) / 8;
+                        xp[0] = nx;
+#pragma unroll
+                        for (int n = 1; n < NT; ++n) xp[n] = n < nt ? column(na, n) : nullptr;
+                    }
+                }
+                if (more) {
+#pragma unroll
+                    for (int i = 0; i < F::kPieces; ++i) x0[i] = x1[i];
+                }
+                a = na;
+                step = nstep;
+            }
+            if (NT == 1)
+                reinterpret_cast<float4*>(area)[batch * 32 + lane] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
+        }
+        group_sync(group, wk);
+        const int me = kw * 32 + lane, threads = wk * 32;
+        if (NT == 1) {
+            for (int i = me; i < batch * 32; i += threads) {
                 float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int v = 0; v < sh.k_warps; ++v) {
-                    const float4 q = group_area[v * kAreaVecs + i];
+                for (int v = 0; v < wk; ++v) {
+                    const float4 q = reinterpret_cast<const float4*>(group_area + v * kAreaFloats)[i];
                     s.x += q.x;
                     s.y += q.y;
                     s.z += q.z;
                     s.w += q.w;
                 }
-                const int64_t flat = 8 * o + (l >> 2);
-                if (flat < lo || flat >= hi) continue;
-                const int64_t row = (o - static_cast<int64_t>(a) * per) * 8 + (l >> 2);
-                const float gate[2] = {s.x, s.y}, up[2] = {s.z, s.w};
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int slot = cm.slot(a, n * 8 + 2 * (l & 3) + c);
-                    if (slot < 0) continue;
-                    const float v = p.ws.share[slot] * (__fdiv_rn(gate[c], 1.0f + expf(-gate[c])) * up[c]);
-                    p.ws.h[static_cast<int64_t>(slot) * p.I + row] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
-                }
+                const int r = lo + (tile0 + (i >> 5) * groups) * 16 + ((i & 31) >> 2), c = 2 * (i & 3);
+                const uint32_t b0 = pack_bf16x2(s.x, s.y), b1 = pack_bf16x2(s.z, s.w);
+                uint16_t* y = p.y + static_cast<int64_t>(c) * p.H + r;
+                if (c < p.m && r < hi) y[0] = static_cast<uint16_t>(b0);
+                if (c + 1 < p.m && r < hi) y[p.H] = static_cast<uint16_t>(b0 >> 16);
+                if (c < p.m && r + 8 < hi) y[8] = static_cast<uint16_t>(b1);
+                if (c + 1 < p.m && r + 8 < hi) y[p.H + 8] = static_cast<uint16_t>(b1 >> 16);
             }
-            group_sync(sh.group, sh.k_warps);
+        } else {
+            const int r0 = lo + tile0 * 16;
+            for (int i = me; i < 16 * p.m; i += threads) {
+                const int r = i & 15, c = i >> 4;
+                float s = 0.f;
+                for (int v = 0; v < wk; ++v) s += group_area[v * kAreaFloats + r * kStride + c];
+                if (r0 + r < hi) p.y[static_cast<int64_t>(c) * p.H + r0 + r] = static_cast<uint16_t>(pack_bf16x2(s, 0.f));
+            }
         }
-        cp_async_wait<0>();
-        __syncthreads();  // the groups of the next phase are others: areas are free
+        group_sync(group, wk);
     }
-    (void)t;
-
-    // ---- down: rows [lo, hi) of y ----
-    const int lo = static_cast<int>(static_cast<int64_t>(p.H) * blockIdx.x / gridDim.x);
-    const int hi = static_cast<int>(static_cast<int64_t>(p.H) * (blockIdx.x + 1) / gridDim.x);
-    stream_rows<F, NT, true>(p.down, p.H, lo, hi, A, L.act, cm, p.ws.h, p.I, p.m, p.y, p.H, ring, areas,
-                             [&] { return grid_barrier(p.ws.barrier, p.status, &L.stop); });
+    cp_async_wait<0>();
 }
 
-constexpr size_t kExpertSmem = kStreamWarps * (kRingBytes + kAreaBytes) + sizeof(ExpertLists);
-static_assert(kExpertSmem <= 227 * 1024, "shared memory of a block");
+// FG: the format's form for shared activations (gate and up), FD: for the down phase.
+template <class FG, class FD, int NT>
+__global__ void __launch_bounds__(kStreamThreads, 1) k_moe_experts(const __grid_constant__ ExpertParams<FG> p) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    using M = Smem<NT>;
+    ExpertLists& L = *reinterpret_cast<ExpertLists*>(smem + M::kLists);
+    uint32_t* field = reinterpret_cast<uint32_t*>(smem + M::kFields);
+    const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * kRingBytes;
+    pdl_wait();
+    build_lists<NT>(L, p.ws.ids, p.m * p.top_k, p.top_k, p.E);
+    const Columns cm{L.cols, L.off, L.cnt, p.top_k};
+    const XBuffer xb{smem_u32(smem) + M::kX, static_cast<int>(M::kXBytes), field, field + kMoeMaxTokens};
+    shared_phase<FG, NT>(GateUpJob<FG, NT>(p, L, cm), ring, smem + M::kAreas, xb);
+    __syncthreads();  // the groups of the next phase are others, and its areas lie over the activations
+    down_phase<FD, NT>(p, L, cm, ring, smem + M::kAreas, [&] { return grid_barrier(p.ws.barrier, p.status, &L.stop); });
+}
 
 template <int TB>
 cudaError_t launch_router(const RouterParams& r, cudaStream_t stream) {
@@ -384,25 +582,25 @@ cudaError_t launch_router(const RouterParams& r, cudaStream_t stream) {
     return launch_pdl(k_moe_router<TB>, dim3(clusters * kRouterCluster), dim3(kRouterWarps * 32), 0, stream, r);
 }
 
-template <class F, int NT>
-cudaError_t launch_experts(const ExpertParams<F>& p, cudaStream_t stream) {
+template <class FG, class FD, int NT>
+cudaError_t launch_experts(const ExpertParams<FG>& p, cudaStream_t stream) {
     static std::atomic<int> configured[64];
-    cudaError_t e = ensure_dynamic_smem(k_moe_experts<F, NT>, kExpertSmem, configured);
+    cudaError_t e = ensure_dynamic_smem(k_moe_experts<FG, FD, NT>, Smem<NT>::kTotal, configured);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(device_info().sm_count));
     cfg.blockDim = dim3(kStreamThreads);
-    cfg.dynamicSmemBytes = kExpertSmem;
+    cfg.dynamicSmemBytes = Smem<NT>::kTotal;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;  // the grid barrier needs every block resident
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_moe_experts<F, NT>, p);
+    return cudaLaunchKernelEx(&cfg, k_moe_experts<FG, FD, NT>, p);
 }
 
-template <class F, class View>
+template <class FG, class FD, class View>
 cudaError_t launch_moe_any(const MoeCall& c, const View& gate, const View& up, const View& down, cudaStream_t stream) {
     const MoeWorkspace ws = carve(c.workspace, static_cast<int64_t>(c.m) * c.top_k);
     const RouterParams r{static_cast<const uint16_t*>(c.router), static_cast<const uint16_t*>(c.x), c.experts, c.hidden, c.m,
@@ -411,12 +609,12 @@ cudaError_t launch_moe_any(const MoeCall& c, const View& gate, const View& up, c
     // router's weights, so that the clusters still fit the SMs at once
     cudaError_t e = c.m <= 16 ? launch_router<1>(r, stream) : (c.m <= 32 ? launch_router<2>(r, stream) : launch_router<4>(r, stream));
     if (e != cudaSuccess) return e;
-    const ExpertParams<F> p{F::make(gate), F::make(up), F::make(down), static_cast<const uint16_t*>(c.x),
+    const ExpertParams<FG> p{FG::make(gate), FG::make(up), FD::make(down), static_cast<const uint16_t*>(c.x),
                             static_cast<uint16_t*>(c.y), c.experts, c.hidden, c.inter, c.m, c.top_k, ws, device_status_ptr()};
-    if (c.m <= 8) return launch_experts<F, 1>(p, stream);
-    if (c.m <= 16) return launch_experts<F, 2>(p, stream);
-    if (c.m <= 32) return launch_experts<F, 4>(p, stream);
-    return launch_experts<F, 8>(p, stream);
+    if (c.m <= 8) return launch_experts<FG, FD, 1>(p, stream);
+    if (c.m <= 16) return launch_experts<FG, FD, 2>(p, stream);
+    if (c.m <= 32) return launch_experts<FG, FD, 4>(p, stream);
+    return launch_experts<FG, FD, 8>(p, stream);
 }
 
 }  // namespace
@@ -427,12 +625,12 @@ size_t moe_workspace_bytes(int64_t inter, int64_t slots) {
 
 cudaError_t launch_moe(const MoeCall& c, const WeightView& gate, const WeightView& up, const WeightView& down,
                        cudaStream_t stream) {
-    return launch_moe_any<Q8Fmt>(c, gate, up, down, stream);
+    return launch_moe_any<Q8Fmt, Q8Fmt>(c, gate, up, down, stream);
 }
 
 cudaError_t launch_mx4_moe(const MoeCall& c, const Mx4View& gate, const Mx4View& up, const Mx4View& down,
                            cudaStream_t stream) {
-    return launch_moe_any<Mx4Fmt>(c, gate, up, down, stream);
+    return launch_moe_any<Mx4HalfFmt, Mx4Fmt>(c, gate, up, down, stream);
 }
 
 }  // namespace mlxq
