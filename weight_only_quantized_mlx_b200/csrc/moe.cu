@@ -178,71 +178,85 @@ struct ExpertParams {
     unsigned int* status;
 };
 
-// Which activation rows an expert's MMA columns hold.  A slot is token * top_k
-// + choice.  Up to 8 tokens (NT == 1): column = token, eight entries per expert,
-// -1 where the token did not choose it.  Otherwise the expert's slots one after
-// another, padded with -1 to a multiple of 8.
+// The hit experts with their tokens, as entries of up to kMaxCols columns (an
+// expert with more tokens takes several entries: its weights are then streamed
+// once for each).  A slot is token * top_k + choice.  Up to 8 tokens (NT == 1):
+// column = token, eight columns per entry, -1 where the token did not choose the
+// expert.  Otherwise an entry's slots one after another, padded with -1 to a
+// multiple of 8.
+constexpr int kMaxCols = 32;
+constexpr int kMaxSlots = kMoeMaxTokens * kMoeMaxTopK;
+constexpr int kMaxEntries = kMaxExperts + kMaxSlots / kMaxCols;
+constexpr int kMaxListed = kMaxSlots + 7 * kMaxExperts;  // lists padded to multiples of 8
+
+struct ExpertLists {
+    int count[kMaxExperts];      // tokens of expert e
+    int place[kMaxExperts];      // first column of expert e, then its next free one
+    int16_t act[kMaxEntries];    // expert of entry a
+    int16_t off[kMaxEntries];    // its first column
+    int16_t cnt[kMaxEntries];    // its columns
+    int16_t cols[kMaxListed];    // slots
+    int entries;
+    int stop;
+};
+
 struct Columns {
     const int16_t* cols;
-    const int16_t* off;  // first entry of active expert a
+    const int16_t* off;
     const int16_t* cnt;
     int top_k;
     __device__ __forceinline__ int slot(int a, int c) const { return cols[off[a] + c]; }
 };
 
-constexpr int kMaxSlots = kMoeMaxTokens * kMoeMaxTopK;
-constexpr int kMaxCols = kMaxSlots + 7 * kMaxExperts;  // lists padded to multiples of 8
-
-struct ExpertLists {
-    int count[kMaxExperts];   // tokens of expert e
-    int place[kMaxExperts];   // NT > 1: next free entry of expert e's list
-    int16_t index[kMaxExperts];  // active index of expert e
-    int16_t act[kMaxExperts];    // expert of active index a
-    int16_t off[kMaxExperts];
-    int16_t cnt[kMaxExperts];
-    int16_t cols[kMaxCols];
-    int experts;
-    int stop;
-};
-
-// All threads of the block.  The order of a list's entries has no effect on
-// results (MMA columns are independent); the experts are in ascending order.
+// All threads of the block.  Entries are in ascending order of experts.  The
+// order of an entry's columns has no effect on results (MMA columns are
+// independent), so they are placed by atomics; which entry of several a token
+// falls into could change the order of sums, so there a slot's place is its rank.
 template <int NT>
 __device__ __forceinline__ void build_lists(ExpertLists& L, const int* ids, int slots, int top_k, int E) {
     const int tid = threadIdx.x, lane = tid & 31;
-    for (int e = tid; e < kMaxExperts; e += kStreamThreads) L.count[e] = 0;
-    for (int c = tid; c < kMaxCols; c += kStreamThreads) L.cols[c] = -1;
+    for (int e = tid; e < E; e += kStreamThreads) L.count[e] = 0;
+    for (int c = tid; c < kMaxListed; c += kStreamThreads) L.cols[c] = -1;
     __syncthreads();
     for (int s = tid; s < slots; s += kStreamThreads) atomicAdd(&L.count[ids[s]], 1);
     __syncthreads();
-    if (tid < 32) {  // exclusive sums over the experts: active index and list start
+    if (tid < 32) {  // exclusive sums over the experts: first entry and first column
         int a = 0, o = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
             const int e = e0 + lane;
             const int n = e < E ? L.count[e] : 0;
-            const unsigned hit = __ballot_sync(0xFFFFFFFFu, n > 0);
-            int len = n > 0 ? (NT == 1 ? 8 : (n + 7) / 8 * 8) : 0, sum = len;
+            const int own = (n + kMaxCols - 1) / kMaxCols, len = n > 0 ? (NT == 1 ? 8 : (n + 7) / 8 * 8) : 0;
+            int sum = len << 16 | own;  // both at once; columns < 2^15, entries < 2^16
+            const int mine = sum;
             for (int d = 1; d < 32; d <<= 1) {
                 const int v = __shfl_up_sync(0xFFFFFFFFu, sum, d);
                 if (lane >= d) sum += v;
             }
-            if (n > 0) {
-                const int i = a + __popc(hit & ((1u << lane) - 1u));
-                L.index[e] = static_cast<int16_t>(i);
-                L.act[i] = static_cast<int16_t>(e);
-                L.off[i] = static_cast<int16_t>(o + sum - len);
-                L.cnt[i] = static_cast<int16_t>(n);
-                L.place[e] = o + sum - len;
+            const int i = a + ((sum - mine) & 0xFFFF), c = o + ((sum - mine) >> 16);
+            for (int j = 0; j < own; ++j) {
+                L.act[i + j] = static_cast<int16_t>(e);
+                L.off[i + j] = static_cast<int16_t>(c + j * kMaxCols);
+                L.cnt[i + j] = static_cast<int16_t>(min(n - j * kMaxCols, kMaxCols));
             }
-            a += __popc(hit);
-            o += __shfl_sync(0xFFFFFFFFu, sum, 31);
+            if (n > 0) L.place[e] = c;
+            const int total = __shfl_sync(0xFFFFFFFFu, sum, 31);
+            a += total & 0xFFFF;
+            o += total >> 16;
         }
-        if (lane == 0) L.experts = a;
+        if (lane == 0) L.entries = a;
     }
     __syncthreads();
     for (int s = tid; s < slots; s += kStreamThreads) {
         const int e = ids[s];
-        const int c = NT == 1 ? L.off[L.index[e]] + s / top_k : atomicAdd(&L.place[e], 1);
+        int c;
+        if (NT == 1) {
+            c = L.place[e] + s / top_k;
+        } else if (L.count[e] <= kMaxCols) {
+            c = atomicAdd(&L.place[e], 1);
+        } else {
+            c = L.place[e];
+            for (int q = 0; q < s; ++q) c += ids[q] == e;
+        }
         L.cols[c] = static_cast<int16_t>(s);
     }
     __syncthreads();
@@ -279,7 +293,8 @@ __device__ __forceinline__ bool grid_barrier(unsigned int* count, unsigned int* 
 //                              | down: areas.
 template <int NT>
 struct Smem {
-    static constexpr uint32_t kDownArea = NT == 1 ? 2048 : 16 * (8 * NT + 4) * 4;  // a warp's sums of the down phase
+    static constexpr int kTokens = NT == 1 ? 8 : (NT == 2 ? 16 : kMoeMaxTokens);  // most tokens of a call
+    static constexpr uint32_t kDownArea = NT == 1 ? 2048 : 16 * (kTokens + 4) * 4;  // a warp's sums of the down phase
     static constexpr uint32_t kLists = kStreamWarps * kRingBytes;
     static constexpr uint32_t kAreas = (kLists + sizeof(ExpertLists) + 127) / 128 * 128;
     static constexpr uint32_t kFields = kAreas + kStreamWarps * kSharedArea;
@@ -306,7 +321,7 @@ struct GateUpJob {
 
     __device__ __forceinline__ GateUpJob(const ExpertParams<F>& p_, const ExpertLists& L_, const Columns& cm_)
         : p(p_), mat(p_.gate), L(L_), cm(cm_) {
-        const int64_t rows = static_cast<int64_t>(L.experts) * p.I;
+        const int64_t rows = static_cast<int64_t>(L.entries) * p.I;
         lo = rows * blockIdx.x / gridDim.x;
         hi = rows * (blockIdx.x + 1) / gridDim.x;
         K = p.H;
@@ -323,12 +338,12 @@ struct GateUpJob {
         const int token = NT == 1 ? c : cm.slot(a_first + s, c) / p.top_k;
         return p.x + static_cast<int64_t>(token) * p.H;
     }
-    __device__ __forceinline__ typename F::Feed feed(int tile, int lane) const {
+    __device__ __forceinline__ void start(typename F::Feed& f, int tile, int lane, int step) const {
         const int o = o0 + tile, a = o / per, g = lane >> 2;
         const int64_t row = static_cast<int64_t>(L.act[a]) * p.I + (o - a * per) * 8 + g;
         const int64_t flat = 8 * static_cast<int64_t>(o) + g;
         const bool live = flat >= lo && flat < hi;
-        return F::feed(p.gate, p.up, row, row, live, live, lane);
+        F::start(f, p.gate, p.up, row, row, live, live, lane, step);
     }
     __device__ __forceinline__ uint32_t key(int tile, int lane) const {
         const int o = o0 + tile, a = o / per;
@@ -368,56 +383,59 @@ __device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int lo = static_cast<int>(static_cast<int64_t>(p.H) * blockIdx.x / gridDim.x);
     const int hi = static_cast<int>(static_cast<int64_t>(p.H) * (blockIdx.x + 1) / gridDim.x);
-    const int tiles = (hi - lo + 15) / 16, S = (p.I + F::kStepCols - 1) / F::kStepCols, A = L.experts, all = A * S;
-    int wk = 1, best = 0x7FFFFFFF;
-    for (int k = 1; k <= kStreamWarps; k *= 2) {
-        const int groups = kStreamWarps / k, cost = (tiles + groups - 1) / groups * ((all + k - 1) / k + (k > 1 ? 2 : 0));
-        if (cost < best) {
-            best = cost;
-            wk = k;
-        }
+    const int tiles = (hi - lo + 15) / 16, S = (p.I + F::kStepCols - 1) / F::kStepCols, A = L.entries;
+    // The warps of a tile (2^lw) split the experts into contiguous ranges and,
+    // 2^ls of them together, the steps of an expert in turns: turns bring
+    // neighbouring 64-byte pieces of a row at about the same time (four or more
+    // warps: whole DRAM bursts; copies alone measured 6 TB/s, against 2.9 with one
+    // warp walking a row), ranges change expert seldom.  Lane i weighs one pair:
+    // steps, about one for a change of expert, two for a join, and an eighth more
+    // below four turns.
+    int lw, ls;
+    {
+        const int i = min(lane, 14), w = i < 1 ? 0 : (i < 3 ? 1 : (i < 6 ? 2 : (i < 10 ? 3 : 4))), d = i - w * (w + 1) / 2;
+        const int rounds = (tiles + (kStreamWarps >> w) - 1) >> (4 - w), ranges = 1 << (w - d);
+        int cost = rounds * (((A + ranges - 1) >> (w - d)) * (((S + (1 << d) - 1) >> d) + 1) + (w > 0 ? 2 : 0));
+        if (d < 2) cost += cost / 8;
+        const uint32_t best = __reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(min(cost, 0x07FFFFFF)) << 4 | static_cast<uint32_t>(i)) & 15u;
+        lw = __shfl_sync(0xFFFFFFFFu, w, static_cast<int>(best));
+        ls = __shfl_sync(0xFFFFFFFFu, d, static_cast<int>(best));
     }
-    const int groups = kStreamWarps / wk, group = warp / wk, kw = warp - group * wk;
-    // This warp's steps of every tile: a contiguous range of all experts' steps,
-    // so that it changes expert (new rows of h, sums to put away) as seldom as can be.
-    const int first = static_cast<int>(static_cast<int64_t>(all) * kw / wk);
-    const int own = static_cast<int>(static_cast<int64_t>(all) * (kw + 1) / wk) - first;
-    const int a0 = first / S, s0 = first % S;
-    int left = own;  // steps of ptile still to be issued
+    const int wk = 1 << lw, groups = kStreamWarps >> lw, group = warp >> lw, kw = warp & (wk - 1);
+    const int turns = 1 << ls, s0 = kw & (turns - 1);
+    const int a0 = A * (kw >> ls) >> (lw - ls), a1 = A * ((kw >> ls) + 1) >> (lw - ls);  // this warp's experts
+    const bool idle = a0 >= a1 || s0 >= S;
     constexpr int kBatch = NT == 1 ? 4 : 1;           // tiles between two joins
     constexpr int kAreaFloats = Smem<NT>::kDownArea / 4;
-    constexpr int kStride = NT * 8 + 1;               // NT > 1: floats per row of the area
+    constexpr int kStride = Smem<NT>::kTokens + 1;    // NT > 1: floats per row of the area
     float* area = reinterpret_cast<float*>(areas + warp * Smem<NT>::kDownArea);
     const float* group_area = reinterpret_cast<const float*>(areas + group * wk * Smem<NT>::kDownArea);
 
-    int ptile = own ? group : tiles, pa = a0, pstep = s0;
-    uint32_t pslot = 0, cslot = 0;
+    int ptile = idle ? tiles : group, pa = a0, pstep = s0;
+    uint32_t pslot = ring, cslot = ring;
     typename F::Feed feed;
-    auto refeed = [&]() {
+    auto restart = [&]() {
         if (ptile >= tiles) return;
         const int r = lo + ptile * 16 + g;
         const int64_t row = static_cast<int64_t>(L.act[pa]) * p.H + r;
-        feed = F::feed(p.down, p.down, row, row + 8, r < hi, r + 8 < hi, lane);
+        F::start(feed, p.down, p.down, row, row + 8, r < hi, r + 8 < hi, lane, s0);
     };
-    refeed();
+    restart();
     auto issue = [&]() {
         if (ptile < tiles) {
-            F::issue(p.down, feed, ring + pslot * kStageBytes, lane, pstep);
-            ++pstep;
-            if (--left == 0) {
-                left = own;
-                pa = a0;
+            F::issue(p.down, feed, pslot, lane, turns);
+            pstep += turns;
+            if (pstep >= S) {
                 pstep = s0;
-                ptile += groups;
-                refeed();
-            } else if (pstep == S) {
-                pstep = 0;
-                ++pa;
-                refeed();
+                if (++pa == a1) {
+                    pa = a0;
+                    ptile += groups;
+                }
+                restart();
             }
         }
         cp_async_commit();
-        pslot = pslot + 1 == kDepth ? 0 : pslot + 1;
+        pslot = pslot == ring + kRingBytes - kStageBytes ? ring : pslot + kStageBytes;
     };
 #pragma unroll 1
     for (int i = 0; i < kDepth - 1; ++i) issue();
@@ -463,6 +481,7 @@ __device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L
                 const int s = cm.slot(a, n * 8 + g);
                 return s >= 0 ? p.ws.h + static_cast<int64_t>(s) * p.I + t * (8 * F::kPieces) : nullptr;
             };
+            // pieces of the lane's row of h for a step; zeros where there is none
             auto fetch = [&](uint4 (&v)[F::kPieces], const uint16_t* row, int step) {
                 const int k = step * F::kStepCols;
                 const bool in = row != nullptr && k + t * (8 * F::kPieces) < p.I;
@@ -472,55 +491,48 @@ __device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L
                     if (in) v[i] = ldg128(row + k + 8 * i);
                 }
             };
-            int a = a0, step = s0, nt = NT == 1 || own == 0 ? 1 : (cm.cnt[a] + 7) / 8;
             uint4 x0[F::kPieces];
-            if (own) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    if (n < nt) xp[n] = column(a, n);
-                fetch(x0, xp[0], step);
+            const uint16_t* row0 = nullptr;  // h of column tile 0
+            if (!idle) {
+                row0 = column(a0, 0);
+                fetch(x0, row0, s0);
             }
-            for (int it = 0; it < own; ++it) {
-                // the step after this one
-                int na = a, nstep = step + 1;
-                if (nstep == S) {
-                    nstep = 0;
-                    ++na;
-                }
-                const bool more = it + 1 < own, turn = more && na != a;
-                const uint16_t* nx = xp[0];
-                if (turn) nx = column(na, 0);
-                uint4 x1[F::kPieces];
-                if (more) fetch(x1, nx, nstep);
+            for (int a = a0; a < a1 && !idle; ++a) {
+                const int nt = NT == 1 ? 1 : (cm.cnt[a] + 7) / 8;
+#pragma unroll
+                for (int n = 1; n < NT; ++n) xp[n] = n < nt ? column(a, n) : nullptr;
                 const uint32_t key = F::row_key(p.down, static_cast<uint32_t>(L.act[a]) * static_cast<uint32_t>(p.H) +
                                                             static_cast<uint32_t>(lo + tile * 16 + g));
-                cp_async_wait<kDepth - 2>();
-                __syncwarp();  // the quad's scales have landed; the slot refilled below is read out
-                issue();
-                const int k = step * F::kStepCols;
-                const bool in = k + t * (8 * F::kPieces) < p.I;
-                F::template consume<NT>(p.down, ring + cslot * kStageBytes, lane, key, step, nt, acc, [&](int i, int n) {
-                    if (n == 0) return x0[i];
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (xp[n] != nullptr && in) v = ldg128(xp[n] + k + 8 * i);
-                    return v;
-                });
-                cslot = cslot + 1 == kDepth ? 0 : cslot + 1;
-                if (turn || !more) {
-                    if (NT > 1) scatter(a, nt);
-                    if (turn) {
-                        nt = NT == 1 ? 1 : (cm.cnt[na] + 7) / 8;
-                        xp[0] = nx;
+                const uint16_t* next0 = a + 1 < a1 ? column(a + 1, 0) : nullptr;
+                // N column tiles, a power of two: unused ones are zeros
+                auto run = [&](auto count) {
+                    constexpr int N = decltype(count)::value < NT ? decltype(count)::value : NT;
+#pragma unroll 1
+                    for (int step = s0; step < S; step += turns) {
+                        const bool turn = step + turns >= S;
+                        uint4 x1[F::kPieces];
+                        fetch(x1, turn ? next0 : row0, turn ? s0 : step + turns);
+                        cp_async_wait<kDepth - 2>();
+                        __syncwarp();  // the copies of all lanes have landed; the slot refilled below is read out
+                        issue();
+                        const int k = step * F::kStepCols;
+                        const bool in = k + t * (8 * F::kPieces) < p.I;
+                        F::template consume<NT, N>(p.down, cslot, lane, key, step, acc, [&](int i, int n) {
+                            if (n == 0) return x0[i];
+                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                            if (xp[n] != nullptr && in) v = ldg128(xp[n] + k + 8 * i);
+                            return v;
+                        });
+                        cslot = cslot == ring + kRingBytes - kStageBytes ? ring : cslot + kStageBytes;
 #pragma unroll
-                        for (int n = 1; n < NT; ++n) xp[n] = n < nt ? column(na, n) : nullptr;
+                        for (int i = 0; i < F::kPieces; ++i) x0[i] = x1[i];
                     }
-                }
-                if (more) {
-#pragma unroll
-                    for (int i = 0; i < F::kPieces; ++i) x0[i] = x1[i];
-                }
-                a = na;
-                step = nstep;
+                };
+                if (NT == 1 || nt == 1) run(std::integral_constant<int, 1>{});
+                else if (NT == 2 || nt == 2) run(std::integral_constant<int, 2>{});
+                else run(std::integral_constant<int, 4>{});
+                row0 = next0;
+                if (NT > 1) scatter(a, nt);
             }
             if (NT == 1)
                 reinterpret_cast<float4*>(area)[batch * 32 + lane] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
@@ -613,8 +625,7 @@ cudaError_t launch_moe_any(const MoeCall& c, const View& gate, const View& up, c
                             static_cast<uint16_t*>(c.y), c.experts, c.hidden, c.inter, c.m, c.top_k, ws, device_status_ptr()};
     if (c.m <= 8) return launch_experts<FG, FD, 1>(p, stream);
     if (c.m <= 16) return launch_experts<FG, FD, 2>(p, stream);
-    if (c.m <= 32) return launch_experts<FG, FD, 4>(p, stream);
-    return launch_experts<FG, FD, 8>(p, stream);
+    return launch_experts<FG, FD, 4>(p, stream);
 }
 
 }  // namespace

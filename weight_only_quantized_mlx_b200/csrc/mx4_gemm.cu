@@ -32,9 +32,9 @@ struct GemmJob {
     __device__ __forceinline__ int end(int) const { return (hi - lo + 15) / 16; }
     __device__ __forceinline__ int cols(int) const { return p.m; }
     __device__ __forceinline__ const uint16_t* x_row(int, int c) const { return p.x + static_cast<int64_t>(c) * p.K; }
-    __device__ __forceinline__ Mx4HalfFmt::Feed feed(int tile, int lane) const {
+    __device__ __forceinline__ void start(Mx4HalfFmt::Feed& f, int tile, int lane, int step) const {
         const int r = lo + tile * 16 + (lane >> 2);
-        return Mx4HalfFmt::feed(p.w, p.w, r, r + 8, r < hi, r + 8 < hi, lane);
+        Mx4HalfFmt::start(f, p.w, p.w, r, r + 8, r < hi, r + 8 < hi, lane, step);
     }
     __device__ __forceinline__ uint32_t key(int tile, int lane) const {
         return Mx4HalfFmt::row_key(p.w, static_cast<uint32_t>(lo + tile * 16 + (lane >> 2)));

@@ -17,6 +17,8 @@
 // row pair fetch what the quad needs.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.cuh"
 #include "kernels.h"
 #include "mx4_common.cuh"
@@ -30,7 +32,7 @@ constexpr uint32_t kStageBytes = 512 + 512 + 128;  // codes of half A, of half B
 constexpr uint32_t kRingBytes = kDepth * kStageBytes;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -82,21 +84,22 @@ struct Q8Fmt {
 
     static __device__ __forceinline__ int group(const Mat& w, int step) { return (step * 64) >> w.log_gs; }
 
-    // Where a lane copies a tile from.  Lane t of a quad also copies table
-    // entries: 0 scale A, 1 bias A, 2 scale B, 3 bias B.  An entry sits in one
-    // half of an aligned 4-byte word (group size 32: the step's two groups are
-    // the two halves; G is even there).
+    // Where a lane copies a tile from, at the present step.  Lane t of a quad also
+    // copies table entries: 0 scale A, 1 bias A, 2 scale B, 3 bias B.  An entry
+    // sits in one half of an aligned 4-byte word (group size 32: the step's two
+    // groups are the two halves; G is even there).  A dead half walks the
+    // matrix's first row and reads no bytes of it.
     struct Feed {
         const uint8_t *a, *b, *table;
         uint32_t na, nb, nt;  // bytes to read: 16 or 0, 4 or 0
         uint32_t odd;         // parity of the row's first table entry
+        int step;
     };
-    static __device__ __forceinline__ Feed feed(const Mat& wa, const Mat& wb, int64_t row_a, int64_t row_b, bool live_a,
-                                                bool live_b, int lane) {
-        const int t = lane & 3;
-        Feed f;
-        f.a = wa.codes + (live_a ? row_a * wa.row_bytes + 16 * t : 0);
-        f.b = wb.codes + (live_b ? row_b * wb.row_bytes + 16 * t : 0);
+    static __device__ __forceinline__ void start(Feed& f, const Mat& wa, const Mat& wb, int64_t row_a, int64_t row_b, bool live_a,
+                                                 bool live_b, int lane, int step) {
+        const int t = lane & 3, off = step * 64 + 16 * t;
+        f.a = wa.codes + (live_a ? row_a * wa.row_bytes : 0) + off;
+        f.b = wb.codes + (live_b ? row_b * wb.row_bytes : 0) + off;
         f.na = live_a ? 16u : 0u;
         f.nb = live_b ? 16u : 0u;
         const bool live = (t & 2) ? live_b : live_a;
@@ -104,25 +107,27 @@ struct Q8Fmt {
         f.odd = static_cast<uint32_t>(e) & 1u;
         f.table = reinterpret_cast<const uint8_t*>(((t & 2) ? wb.tables[t & 1] : wa.tables[t & 1]) + (e - f.odd));
         f.nt = live ? 4u : 0u;
-        return f;
+        f.step = step;
     }
-    static __device__ __forceinline__ void issue(const Mat& w, const Feed& f, uint32_t slot, int lane, int step) {
-        // a dead half points at the matrix's first row and reads no bytes of it
-        const uint32_t off = static_cast<uint32_t>(step) * 64u;
+    // Copy the step into the stage at slot and go on by `by` steps.
+    static __device__ __forceinline__ void issue(const Mat& w, Feed& f, uint32_t slot, int lane, int by) {
         const uint32_t dst = slot + static_cast<uint32_t>(lane) * 16u;
-        cp_async16(dst, f.a + off, f.na);
-        cp_async16(dst + 512u, f.b + off, f.nb);
-        const uint32_t e = (f.odd + static_cast<uint32_t>(group(w, step))) >> 1;
-        cp_async4(slot + 1024u + static_cast<uint32_t>(lane) * 4u, f.table + 4u * e, f.nt);
+        cp_async16(dst, f.a, f.na);
+        cp_async16(dst + 512u, f.b, f.nb);
+        const uint32_t e = (f.odd + static_cast<uint32_t>(group(w, f.step))) >> 1;
+        cp_async4(dst + 1024u - static_cast<uint32_t>(lane) * 12u, f.table + 4u * e, f.nt);
+        f.a += by * 64;
+        f.b += by * 64;
+        f.step += by;
     }
 
     // What a lane needs to read its scales: the parity of its row's first entry.
     static __device__ __forceinline__ uint32_t row_key(const Mat& w, uint32_t row) { return row & static_cast<uint32_t>(w.G) & 1u; }
 
-    // One step: acc[n] += W(16 rows) x(8 columns n) over the step's k.  x(i, n):
-    // this lane's piece i of column tile n.
-    template <int NT, class X>
-    static __device__ __forceinline__ void consume(const Mat& w, uint32_t slot, int lane, uint32_t key, int step, int nt,
+    // One step: acc[n] += W(16 rows) x(8 columns n), n < N, over the step's k.
+    // x(i, n): this lane's piece i of column tile n.
+    template <int NT, int N, class X>
+    static __device__ __forceinline__ void consume(const Mat& w, uint32_t slot, int lane, uint32_t key, int step,
                                                    float (&acc)[NT][4], X x) {
         const int t = lane & 3;
         const uint4 ca = lds128(slot + static_cast<uint32_t>(lane) * 16u);
@@ -145,8 +150,7 @@ struct Q8Fmt {
                 a[j][3] = pair<2>(wb[2 * i + j], sb2, bb2);
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (n >= nt) break;
+            for (int n = 0; n < N; ++n) {
                 const uint4 v = x(i, n);
                 mma_bf16(acc[n], a[0][0], a[0][1], a[0][2], a[0][3], v.x, v.y);
                 mma_bf16(acc[n], a[1][0], a[1][1], a[1][2], a[1][3], v.z, v.w);
@@ -168,12 +172,12 @@ struct Q8Fmt {
     static constexpr bool kScaled = false;
     static __device__ __forceinline__ int piece_index(int r) { return r % kPieces; }
     static __device__ __forceinline__ int piece_lane(int r) { return r / kPieces; }
-    template <int NT>
-    static __device__ __forceinline__ void consume_shared(const Mat& w, uint32_t slot, int lane, uint32_t key, int step, int nt,
+    template <int NT, int N>
+    static __device__ __forceinline__ void consume_shared(const Mat& w, uint32_t slot, int lane, uint32_t key, int step,
                                                           float (&acc)[NT][4], uint32_t x, uint32_t piece_stride,
                                                           const uint32_t (&xo)[NT], bool&, const uint32_t*, int) {
-        consume<NT>(w, slot, lane, key, step, nt, acc,
-                    [&](int i, int n) { return lds128(x + static_cast<uint32_t>(i) * piece_stride + xo[n]); });
+        consume<NT, N>(w, slot, lane, key, step, acc,
+                       [&](int i, int n) { return lds128(x + static_cast<uint32_t>(i) * piece_stride + xo[n]); });
     }
 };
 
@@ -199,35 +203,39 @@ struct Mx4Fmt {
     // the table left out.  The last step of a row may be short.
     struct Feed {
         const uint8_t *a, *b, *table;
-        int ca, cb;  // codes left in the row from the lane's first byte
+        int ca, cb;  // bytes of codes from the lane's first one to the row's end
         int ct;      // scale bytes left in the table
     };
-    static __device__ __forceinline__ Feed feed(const Mat& wa, const Mat& wb, int64_t row_a, int64_t row_b, bool live_a,
-                                                bool live_b, int lane) {
-        const int t = lane & 3;
-        Feed f;
-        f.a = wa.codes + (live_a ? row_a * wa.row_bytes + 16 * t : 0);
-        f.b = wb.codes + (live_b ? row_b * wb.row_bytes + 16 * t : 0);
-        f.ca = live_a ? static_cast<int>(wa.row_bytes) - 16 * t : 0;
-        f.cb = live_b ? static_cast<int>(wa.row_bytes) - 16 * t : 0;
+    static __device__ __forceinline__ void start(Feed& f, const Mat& wa, const Mat& wb, int64_t row_a, int64_t row_b, bool live_a,
+                                                 bool live_b, int lane, int step) {
+        const int t = lane & 3, off = step * 64 + 16 * t;
+        f.a = wa.codes + (live_a ? row_a * wa.row_bytes : 0) + off;
+        f.b = wb.codes + (live_b ? row_b * wb.row_bytes : 0) + off;
+        f.ca = live_a ? static_cast<int>(wa.row_bytes) - off : 0;
+        f.cb = live_b ? static_cast<int>(wa.row_bytes) - off : 0;
         const bool live = (t & 2) ? live_b : live_a;
         // (a dead half reads the first row's scales: any will do, its codes are zeros)
-        const int64_t e = (live ? (((t & 2) ? row_b : row_a) * wa.G) & ~int64_t{3} : 0) + 4 * (t & 1);
+        const int64_t e = (live ? (((t & 2) ? row_b : row_a) * wa.G) & ~int64_t{3} : 0) + 4 * (t & 1) + 4 * step;
         const int64_t left = wa.scale_bytes - e;
-        f.table = ((t & 2) ? wb.scales : wa.scales) + (left > 0 ? e : 0);
-        f.ct = left > 0x40000000 ? 0x40000000 : (left > 0 ? static_cast<int>(left) : 0);
-        return f;
+        f.table = ((t & 2) ? wb.scales : wa.scales) + e;
+        f.ct = left > 0x40000000 ? 0x40000000 : static_cast<int>(left);
     }
-    static __device__ __forceinline__ void issue(const Mat& w, const Feed& f, uint32_t slot, int lane, int step) {
-        (void)w;
-        const int off = step * 64;
+    // Copy the step into the stage at slot and go on by `by` steps.  (A copy of no
+    // bytes does not touch its source, which may lie behind the matrix.)
+    static __device__ __forceinline__ void issue_at(Feed& f, uint32_t dst, uint32_t tdst, int by) {
+        cp_async16(dst, f.a, f.ca > 0 ? 16u : 0u);
+        cp_async16(dst + 512u, f.b, f.cb > 0 ? 16u : 0u);
+        cp_async4(tdst, f.table, static_cast<uint32_t>(min(max(f.ct, 0), 4)));
+        f.a += by * 64;
+        f.b += by * 64;
+        f.table += by * 4;
+        f.ca -= by * 64;
+        f.cb -= by * 64;
+        f.ct -= by * 4;
+    }
+    static __device__ __forceinline__ void issue(const Mat&, Feed& f, uint32_t slot, int lane, int by) {
         const uint32_t dst = slot + static_cast<uint32_t>(lane) * 16u;
-        const bool ia = off < f.ca, ib = off < f.cb;
-        cp_async16(dst, f.a + (ia ? off : 0), ia ? 16u : 0u);
-        cp_async16(dst + 512u, f.b + (ib ? off : 0), ib ? 16u : 0u);
-        const int left = f.ct - step * 4;
-        cp_async4(slot + 1024u + static_cast<uint32_t>(lane) * 4u, f.table + (left > 0 ? step * 4 : 0),
-                  static_cast<uint32_t>(min(max(left, 0), 4)));
+        issue_at(f, dst, dst + 1024u - static_cast<uint32_t>(lane) * 12u, by);
     }
 
     // the shift that brings a row's first scale byte to the bottom of its first word
@@ -235,8 +243,8 @@ struct Mx4Fmt {
         return 8u * ((row * static_cast<uint32_t>(w.G)) & 3u);
     }
 
-    template <int NT, class X>
-    static __device__ __forceinline__ void consume(const Mat& w, uint32_t slot, int lane, uint32_t key, int step, int nt,
+    template <int NT, int N, class X>
+    static __device__ __forceinline__ void consume(const Mat& w, uint32_t slot, int lane, uint32_t key, int step,
                                                    float (&acc)[NT][4], X x) {
         const int t = lane & 3;
         const uint4 ca = lds128(slot + static_cast<uint32_t>(lane) * 16u);
@@ -271,8 +279,7 @@ struct Mx4Fmt {
                 }
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (n >= nt) break;
+            for (int n = 0; n < N; ++n) {
                 const uint4 v = x(i, n);
                 mma_bf16(acc[n], a[0], b[0], a[1], b[1], v.x, v.y);
                 mma_bf16(acc[n], a[2], b[2], a[3], b[3], v.z, v.w);
@@ -305,16 +312,9 @@ struct Mx4Fmt {
 struct Mx4HalfFmt : Mx4Fmt {
     // the 16-byte unit of block b in row g sits at unit b ^ (g / 2), so that the
     // 32 lanes' word loads (row g, word t) touch 32 banks
-    static __device__ __forceinline__ void issue(const Mat& w, const Feed& f, uint32_t slot, int lane, int step) {
-        (void)w;
-        const int off = step * 64, g = lane >> 2, t = lane & 3;
-        const uint32_t dst = slot + static_cast<uint32_t>(g) * 64u + static_cast<uint32_t>((t ^ (g >> 1)) & 3) * 16u;
-        const bool ia = off < f.ca, ib = off < f.cb;
-        cp_async16(dst, f.a + (ia ? off : 0), ia ? 16u : 0u);
-        cp_async16(dst + 512u, f.b + (ib ? off : 0), ib ? 16u : 0u);
-        const int left = f.ct - step * 4;
-        cp_async4(slot + 1024u + static_cast<uint32_t>(lane) * 4u, f.table + (left > 0 ? step * 4 : 0),
-                  static_cast<uint32_t>(min(max(left, 0), 4)));
+    static __device__ __forceinline__ void issue(const Mat&, Feed& f, uint32_t slot, int lane, int by) {
+        const int g = lane >> 2, t = lane & 3;
+        issue_at(f, slot + static_cast<uint32_t>(g * 64 + ((t ^ (g >> 1)) & 3) * 16), slot + 1024u + static_cast<uint32_t>(lane) * 4u, by);
     }
 
     static constexpr bool kScaled = true;
@@ -325,8 +325,8 @@ struct Mx4HalfFmt : Mx4Fmt {
     // numbers, for the rest of the tile, at the first step with a scale outside
     // 2^-63 .. 2^64: there each product meets scale and unit in the order that
     // does not leave fp32 on the way.
-    template <int NT>
-    static __device__ __forceinline__ void consume_shared(const Mat& w, uint32_t slot, int lane, uint32_t key, int step, int nt,
+    template <int NT, int N>
+    static __device__ __forceinline__ void consume_shared(const Mat& w, uint32_t slot, int lane, uint32_t key, int step,
                                                           float (&acc)[NT][4], uint32_t x, uint32_t piece_stride,
                                                           const uint32_t (&xo)[NT], bool& plain, const uint32_t* field, int cols) {
         const int g = lane >> 2, t = lane & 3;
@@ -347,20 +347,20 @@ struct Mx4HalfFmt : Mx4Fmt {
         float sa[4], sb[4];
         e8m0x4(ea, sa);
         e8m0x4(eb, sb);
-        const uint32_t row = slot + static_cast<uint32_t>(g) * 64u + static_cast<uint32_t>(t) * 4u;
+        // block b of row g, word t: bits 4 and 5 of the address hold b ^ (g / 2)
+        const uint32_t row = slot + static_cast<uint32_t>(g * 64 + ((g >> 1) & 3) * 16 + t * 4);
         if (plain) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                const uint32_t at = row + static_cast<uint32_t>((b ^ (g >> 1)) & 3) * 16u;
+                const uint32_t at = row ^ static_cast<uint32_t>(b * 16);
                 uint32_t a[4], c[4];
                 e2m1x8_f16(lds32(at), a);
                 e2m1x8_f16(lds32(at + 512u), c);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (n >= nt) break;
+                for (int n = 0; n < N; ++n) {
                     const uint4 v = lds128(x + static_cast<uint32_t>(b) * piece_stride + xo[n]);
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_f16(d, a[0], c[0], a[1], c[1], v.x, v.y);
+                    float d[4];
+                    mma_f16_first(d, a[0], c[0], a[1], c[1], v.x, v.y);
                     mma_f16(d, a[2], c[2], a[3], c[3], v.z, v.w);
                     acc[n][0] = __fmaf_rn(d[0], sa[b], acc[n][0]);
                     acc[n][1] = __fmaf_rn(d[1], sa[b], acc[n][1]);
@@ -371,18 +371,17 @@ struct Mx4HalfFmt : Mx4Fmt {
         } else {
 #pragma unroll 1
             for (int b = 0; b < 4; ++b) {
-                const uint32_t at = row + static_cast<uint32_t>((b ^ (g >> 1)) & 3) * 16u;
+                const uint32_t at = row ^ static_cast<uint32_t>(b * 16);
                 uint32_t a[4], c[4];
                 e2m1x8_f16(lds32(at), a);
                 e2m1x8_f16(lds32(at + 512u), c);
                 const float s0 = b == 0 ? sa[0] : (b == 1 ? sa[1] : (b == 2 ? sa[2] : sa[3]));
                 const float s1 = b == 0 ? sb[0] : (b == 1 ? sb[1] : (b == 2 ? sb[2] : sb[3]));
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (n >= nt) break;
+                for (int n = 0; n < N; ++n) {
                     const uint4 v = lds128(x + static_cast<uint32_t>(b) * piece_stride + xo[n]);
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_f16(d, a[0], c[0], a[1], c[1], v.x, v.y);
+                    float d[4];
+                    mma_f16_first(d, a[0], c[0], a[1], c[1], v.x, v.y);
                     mma_f16(d, a[2], c[2], a[3], c[3], v.z, v.w);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -430,6 +429,13 @@ struct Mx4HalfFmt : Mx4Fmt {
         s[1] = __uint_as_float(lo & 0xFFFF0000u);
         s[2] = __uint_as_float(hi << 16);
         s[3] = __uint_as_float(hi & 0xFFFF0000u);
+    }
+    static __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                         uint32_t b0, uint32_t b1) {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
     }
     static __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                                    uint32_t b1) {
@@ -520,7 +526,7 @@ constexpr uint32_t kSharedArea = 2176;  // a warp's partial sums awaiting a join
 
 // Tiles in segments; the tiles of a segment multiply the same columns.  Job:
 //   mat, K, segs; begin(s), end(s): tiles of segment s; cols(s); x_row(s, c);
-//   feed(tile, lane), key(tile, lane): where the lane's rows are;
+//   start(feed, tile, lane, step), key(tile, lane): where the lane's rows are;
 //   store(s, tile, n, lane, v): sums of column tile n in fragment order.
 // All warps of the block call this together.
 template <class F, int NT, class Job>
@@ -529,47 +535,48 @@ __device__ __forceinline__ void shared_phase(const Job& job, uint32_t ring, uint
     const int S = (job.K + F::kStepCols - 1) / F::kStepCols;
     auto chunk_steps = [&](int s) { return min(S, xb.bytes / (64 * F::kPieces * job.cols(s))); };
 
-    // How many warps share a tile's K: the choice that ends first, counting
-    // steps, about two more for joining partial sums and four for a refill of
-    // the activations.
-    int wk = 1, best = 0x7FFFFFFF;
-    for (int k = 1; k <= kStreamWarps; k *= 2) {
+    // How many warps share a tile's K (lane i weighs 2^i): the choice that ends
+    // first, counting steps, about two more for joining partial sums and four
+    // for a refill of the activations.
+    int lw;
+    {
+        const int i = min(lane, 4), k = 1 << i;
         int cost = 0;
         for (int s = 0; s < job.segs; ++s) {
-            const int groups = kStreamWarps / k, tiles = job.end(s) - job.begin(s);
-            const int cs = chunk_steps(s), chunks = (S + cs - 1) / cs;
-            cost += (tiles + groups - 1) / groups * (chunks * ((cs + k - 1) / k) + (k > 1 ? 2 : 0) + (chunks > 1 ? 4 * chunks : 0));
+            const int tiles = job.end(s) - job.begin(s), rounds = (tiles + (kStreamWarps >> i) - 1) >> (4 - i);
+            const int cs = chunk_steps(s), chunks = cs == S ? 1 : (S + cs - 1) / cs;
+            cost += rounds * (chunks * ((cs + k - 1) >> i) + (i > 0 ? 2 : 0) + (chunks > 1 ? 4 * chunks : 0));
         }
-        if (cost < best) {
-            best = cost;
-            wk = k;
-        }
+        lw = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(min(cost, 0x0FFFFFFF)) << 3 | static_cast<uint32_t>(i)) & 7u);
     }
-    const int groups = kStreamWarps / wk, group = warp / wk, kw = warp - group * wk;
+    const int wk = 1 << lw, groups = kStreamWarps >> lw, group = warp >> lw, kw = warp & (wk - 1);
 
-    // producer: segment, tile, step; the same order as the consumer below
-    int ps = 0, ptile = job.segs ? job.begin(0) + group : 0, pstep = kw;
-    uint32_t pslot = 0, cslot = 0;
+    // producer: segment and tile, in the same order as the consumer below
+    int ps = 0, ptile = job.segs ? job.begin(0) + group : 0;
+    const int own = kw < S ? (S - kw + wk - 1) >> lw : 0;  // this warp's steps of a tile
+    int pleft = 0;
+    uint32_t pslot = ring, cslot = ring;
     typename F::Feed feed;
     auto seek = [&]() {  // the next tile of this group at or behind ptile, and its feed
         while (ps < job.segs && ptile >= job.end(ps))
             if (++ps < job.segs) ptile = job.begin(ps) + group;
-        if (ps < job.segs) feed = job.feed(ptile, lane);
-    };
-    if (kw >= S) ps = job.segs;  // no step of any tile is this warp's
-    seek();
-    auto issue = [&]() {
+        pleft = 0;
         if (ps < job.segs) {
-            F::issue(job.mat, feed, ring + pslot * kStageBytes, lane, pstep);
-            pstep += wk;
-            if (pstep >= S) {
-                pstep = kw;
+            job.start(feed, ptile, lane, kw);
+            pleft = own;
+        }
+    };
+    if (own > 0) seek();
+    auto issue = [&]() {
+        if (pleft > 0) {
+            F::issue(job.mat, feed, pslot, lane, wk);
+            if (--pleft == 0) {
                 ptile += groups;
                 seek();
             }
         }
         cp_async_commit();
-        pslot = pslot + 1 == kDepth ? 0 : pslot + 1;
+        pslot = pslot == ring + kRingBytes - kStageBytes ? ring : pslot + kStageBytes;
     };
 #pragma unroll 1
     for (int i = 0; i < kDepth - 1; ++i) issue();
@@ -623,15 +630,25 @@ __device__ __forceinline__ void shared_phase(const Job& job, uint32_t ring, uint
                 if (!live) continue;
                 const int end = min((c + 1) * cs, S);
                 uint32_t x = xb.addr + static_cast<uint32_t>((step - c * cs) * F::kPieces) * piece_stride;
-                for (; step < end; step += wk) {
-                    cp_async_wait<kDepth - 2>();
-                    __syncwarp();  // the copies of all lanes have landed; the slot refilled below is read out
-                    issue();
-                    F::template consume_shared<NT>(job.mat, ring + cslot * kStageBytes, lane, key, step, nt, acc, x, piece_stride, xo, plain,
-                                                   xb.field, cols);
-                    x += static_cast<uint32_t>(wk * F::kPieces) * piece_stride;
-                    cslot = cslot + 1 == kDepth ? 0 : cslot + 1;
-                }
+                const uint32_t x_step = static_cast<uint32_t>(F::kPieces << lw) * piece_stride;
+                // N column tiles, a power of two: unused ones repeat the last column
+                auto run = [&](auto count) {
+                    constexpr int N = decltype(count)::value < NT ? decltype(count)::value : NT;
+#pragma unroll 1
+                    for (; step < end; step += wk) {
+                        cp_async_wait<kDepth - 2>();
+                        __syncwarp();  // the copies of all lanes have landed; the slot refilled below is read out
+                        issue();
+                        F::template consume_shared<NT, N>(job.mat, cslot, lane, key, step, acc, x, piece_stride, xo, plain, xb.field,
+                                                          cols);
+                        x += x_step;
+                        cslot = cslot == ring + kRingBytes - kStageBytes ? ring : cslot + kStageBytes;
+                    }
+                };
+                if (NT == 1 || nt == 1) run(std::integral_constant<int, 1>{});
+                else if (NT == 2 || nt == 2) run(std::integral_constant<int, 2>{});
+                else if (NT == 4 || nt <= 4) run(std::integral_constant<int, 4>{});
+                else run(std::integral_constant<int, 8>{});
             }
             if constexpr (F::kScaled) {
                 if (plain) F::template to_numbers<NT>(acc, xb.field, cols, t);
