@@ -601,6 +601,8 @@ cudaError_t static_scratch_base(int device, unsigned char** out) {
 
 }  // namespace
 
+cudaError_t scratch_pool(int device, cudaMemPool_t* out) { return workspace_pool(device, out); }
+
 // Synchronous: called from mlxq_device_status after a device-wide sync.
 cudaError_t reset_static_scratch_counters() {
     const DeviceInfo& dev = device_info();

@@ -1,9 +1,21 @@
 // Y = X W^T with an MX4 weight and BF16 activations, up to 64 rows of X.
 //
-// HBM-bound on the weight (17/32 bytes per element): one block per SM streams
-// a balanced range of rows of W, every byte once (row_stream.cuh), and keeps the
-// rows of X in shared memory (in chunks of K where they do not fit).  One
-// rounding, of the result.
+// HBM-bound on the weight (17/32 bytes per element): blocks stream balanced
+// ranges of its rows, every byte once (row_stream.cuh).  One rounding, of the
+// result.
+//
+// k_mx4_gemm, up to kDirectRows rows of X: a block keeps them in shared memory,
+// converted on the way (in chunks of K where they do not fit).
+//
+// k_mx4_gemm_async, more rows: every block needs all of X over its columns, and
+// fetching and converting them between products took most of the time (4096 x
+// 4096, m = 64: 80 us).  So k_mx4_prepare writes X once in the order and units in
+// which the products take it, step after step, and bulk copies bring the steps into
+// a ring while the warps multiply.  S blocks of a
+// cluster share a range of rows and split K, which divides the copies of X by S,
+// and add their sums through distributed shared memory in rank order.
+#include <cooperative_groups.h>
+
 #include "row_stream.cuh"
 
 namespace mlxq {
@@ -78,16 +90,377 @@ cudaError_t launch_nt(const GemmParams& p, cudaStream_t stream) {
     return launch_pdl(k_mx4_gemm<NT>, dim3(static_cast<unsigned>(octets < sms ? octets : sms)), dim3(kStreamThreads), kTotal, stream, p);
 }
 
+// ---- more rows ------------------------------------------------------------------------------
+struct AsyncParams {
+    Mx4HalfFmt::Mat w;
+    const uint8_t* xp;      // pieces of X: ((step 4 + block) m + row) 64 + 16 t
+    const uint32_t* field;  // [m]
+    uint16_t* y;
+    int N, K, m, S;
+    unsigned int* status;
+};
+
+constexpr int kAsyncDepth = 4;  // ring stages of a warp: with X in a ring beside them, six leave too little room for it
+constexpr uint32_t kAsyncRing = kAsyncDepth * kStageBytes;
+constexpr uint32_t kAsyncAreas = kStreamWarps * kAsyncRing;
+constexpr uint32_t kAsyncFields = kAsyncAreas + kStreamWarps * kSharedArea;
+constexpr uint32_t kAsyncX = kAsyncFields + kMx4GemmMaxM * 4;
+constexpr uint32_t kPartialBytes = 32 * 1024;  // S > 1: fp32 sums of a cluster's rows
+constexpr int kMaxXStages = 16;
+constexpr uint32_t kAsyncTotal = 227 * 1024 - 512;
+
+// A block per row of X: its unit (the largest exponent), then its pieces.
+constexpr int kPrepareThreads = 512;
+__global__ void __launch_bounds__(kPrepareThreads) k_mx4_prepare(const uint16_t* __restrict__ x, int K, int m, int steps,
+                                                                 uint8_t* __restrict__ xp, uint32_t* __restrict__ fields) {
+    __shared__ uint32_t top;
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) top = 0u;
+    __syncthreads();
+    pdl_wait();
+    const int c = blockIdx.x, pieces = steps * 16;
+    const uint4* src = reinterpret_cast<const uint4*>(x + static_cast<int64_t>(c) * K);
+    uint32_t f = 0;
+    for (int q = threadIdx.x; q < K / 8; q += kPrepareThreads) f = max(f, max_field(__ldg(src + q)));
+    f = __reduce_max_sync(0xFFFFFFFFu, f);
+    if ((threadIdx.x & 31) == 0) atomicMax(&top, f);
+    __syncthreads();
+    f = top;
+    if (threadIdx.x == 0) fields[c] = f;
+    const float inv = __uint_as_float((254u - x_field(f)) << 23);  // 1 / unit
+    for (int q = threadIdx.x; q < pieces; q += kPrepareThreads) {
+        const uint4 v = q < K / 8 ? __ldg(src + q) : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(xp + (static_cast<int64_t>(q >> 2) * m + c) * 64 + (q & 3) * 16) =
+            make_uint4(scaled_half2(v.x, inv), scaled_half2(v.y, inv), scaled_half2(v.z, inv), scaled_half2(v.w, inv));
+    }
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
+    float v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
+                 : "=f"(v)
+                 : "r"(addr), "r"(rank));
+    return v;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kStreamThreads, 1) k_mx4_gemm_async(const __grid_constant__ AsyncParams p) {
+    using F = Mx4HalfFmt;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[2 * kMaxXStages];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    pdl_launch_dependents();
+    const int S = p.S, rank = static_cast<int>(blockIdx.x) % S, cl = static_cast<int>(blockIdx.x) / S;
+    const int clusters = static_cast<int>(gridDim.x) / S;
+    const int lo = static_cast<int>(static_cast<int64_t>(p.N) * cl / clusters);
+    const int hi = static_cast<int>(static_cast<int64_t>(p.N) * (cl + 1) / clusters);
+    const int all_steps = (p.K + F::kStepCols - 1) / F::kStepCols;
+    const int st0 = static_cast<int>(static_cast<int64_t>(all_steps) * rank / S);
+    const int steps = static_cast<int>(static_cast<int64_t>(all_steps) * (rank + 1) / S) - st0;
+    const int tiles = (hi - lo + 15) / 16;
+    const uint32_t step_bytes = static_cast<uint32_t>(p.m) * 256u;
+    const uint32_t partial = smem_u32(smem) + kAsyncX, x0 = partial + (S > 1 ? kPartialBytes : 0u);
+    const int room = min(static_cast<int>((smem_u32(smem) + kAsyncTotal - x0) / step_bytes), kMaxXStages);
+    uint32_t* field = reinterpret_cast<uint32_t*>(smem + kAsyncFields);
+
+    // Warps per tile (lane i weighs 2^i of them): steps, and two for a join.  A
+    // stage of X is one step; their number is a multiple of the warps of a tile,
+    // so that a warp meets a stage only in its own steps (it could else test the
+    // barrier's parity a phase early), and at least twice it.
+    int lw;
+    {
+        const int i = min(lane, 4);
+        int cost = ((tiles + (kStreamWarps >> i) - 1) >> (4 - i)) * (((steps + (1 << i) - 1) >> i) + (i > 0 ? 2 : 0));
+        if ((2 << i) > room && i > 0) cost = 0x0FFFFFFF;
+        lw = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(min(cost, 0x0FFFFFFF)) << 3 | static_cast<uint32_t>(i)) & 7u);
+    }
+    const int wk = 1 << lw, groups = kStreamWarps >> lw, stages = room >> lw << lw;
+    const int rounds = (tiles + groups - 1) / groups;
+    auto full = [&](int s) { return smem_u32(&bars[s]); };
+    auto empty = [&](int s) { return smem_u32(&bars[kMaxXStages + s]); };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), static_cast<uint32_t>(groups));  // the warp of each group whose step it is
+        }
+        mbar_fence_init();
+    }
+    __syncthreads();
+    pdl_wait();
+
+    // (A round has a multiple of wk steps, the last ones perhaps without work, so
+    // that a warp's steps fall on the same stages in every round.)
+    const int padded = (steps + wk - 1) >> lw << lw, total = rounds * padded;
+    const uint64_t pol = policy_evict_last();
+    auto feed_x = [&](int s, int k) {  // step k of a round into stage s
+        mbar_arrive_expect_tx(full(s), step_bytes);
+        bulk_g2s(x0 + static_cast<uint32_t>(s) * step_bytes, p.xp + static_cast<int64_t>(st0 + min(k, steps - 1)) * step_bytes, step_bytes,
+                 full(s), pol);
+    };
+    if (threadIdx.x == 0)
+        for (int it = 0; it < min(stages, total); ++it) feed_x(it, it % padded);
+    __syncwarp();
+    {
+        const int group = warp >> lw, kw = warp & (wk - 1);
+        const uint32_t ring = smem_u32(smem) + warp * kAsyncRing;
+        float4* area = reinterpret_cast<float4*>(smem + kAsyncAreas + warp * kSharedArea);
+        const float4* group_area = reinterpret_cast<const float4*>(smem + kAsyncAreas + group * wk * kSharedArea);
+        constexpr int kAreaVecs = kSharedArea / 16;
+        constexpr int kJoin = NT < 4 ? NT : 4;  // column tiles of a join
+
+        const int own = kw < steps ? (steps - kw + wk - 1) >> lw : 0;
+        int ptile = own > 0 ? group : tiles, pleft = 0;
+        uint32_t pslot = ring, cslot = ring;
+        F::Feed feed;
+        auto seek = [&]() {
+            pleft = 0;
+            if (ptile < tiles) {
+                const int r = lo + ptile * 16 + g;
+                F::start(feed, p.w, p.w, r, r + 8, r < hi, r + 8 < hi, lane, st0 + kw);
+                pleft = own;
+            }
+        };
+        seek();
+        auto issue = [&]() {
+            if (pleft > 0) {
+                F::issue(p.w, feed, pslot, lane, wk);
+                if (--pleft == 0) {
+                    ptile += groups;
+                    seek();
+                }
+            }
+            cp_async_commit();
+            pslot = pslot == ring + kAsyncRing - kStageBytes ? ring : pslot + kStageBytes;
+        };
+#pragma unroll 1
+        for (int i = 0; i < kAsyncDepth - 1; ++i) issue();
+        for (int c = threadIdx.x; c < p.m; c += kStreamThreads) field[c] = p.field[c];
+        __syncthreads();  // the fields are there
+
+        const int nt = (p.m + 7) / 8;
+        const uint32_t piece_stride = static_cast<uint32_t>(p.m) * 64u;
+        uint32_t xo[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) xo[n] = static_cast<uint32_t>(min(n * 8 + g, p.m - 1)) * 64u + static_cast<uint32_t>(t) * 16u;
+        auto store = [&](int tile, int n, int l, const float4& v) {
+            const int r = tile * 16 + (l >> 2), c = n * 8 + 2 * (l & 3), rows = hi - lo;
+            const float s[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = r + (i >> 1) * 8, col = c + (i & 1);
+                if (col >= p.m || row >= rows) continue;
+                if (S > 1)
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(partial + static_cast<uint32_t>(col * rows + row) * 4u), "f"(s[i]) : "memory");
+                else
+                    p.y[static_cast<int64_t>(col) * p.N + lo + row] = static_cast<uint16_t>(pack_bf16x2(s[i], 0.f));
+            }
+        };
+        bool ok = true;
+        int stage = kw;        // of this warp's present step; stages is a multiple of wk
+        uint32_t parity = 0;   // of that stage's use
+        const int ahead = (stages - wk) % padded;
+        for (int r = 0; r < rounds; ++r) {
+            const int tile = r * groups + group;
+            const bool live = tile < tiles;
+            float acc[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+            const uint32_t key = F::row_key(p.w, static_cast<uint32_t>(lo + tile * 16 + g));
+            bool plain = true;  // sums are in the columns' units
+            auto run = [&](auto count) {
+                constexpr int N = decltype(count)::value < NT ? decltype(count)::value : NT;
+#pragma unroll 1
+                for (int k = kw; k < padded; k += wk) {
+                    const int it = r * padded + k;
+                    // The stage of this warp's last step gets its next contents as soon as
+                    // all groups have read it: one warp of each kw sees to it, the groups
+                    // taking turns.
+                    const int next = it + stages - wk;
+                    if (it >= wk && next < total && ((next >> lw) & (groups - 1)) == group && ok) {
+                        const int s = stage >= wk ? stage - wk : stage - wk + stages;
+                        ok = mbar_wait(empty(s), stage >= wk ? parity : parity ^ 1u, p.status);
+                        if (lane == 0 && ok) feed_x(s, k + ahead < padded ? k + ahead : k + ahead - padded);
+                        __syncwarp();
+                    }
+                    // after a wait has given up there are no more, the control flow goes on
+                    if (ok) ok = mbar_wait(full(stage), parity, p.status);
+                    if (live && k < steps) {
+                        cp_async_wait<kAsyncDepth - 2>();
+                        __syncwarp();  // the copies of all lanes have landed; the slot refilled below is read out
+                        issue();
+                        F::consume_shared<NT, N>(p.w, cslot, lane, key, st0 + k, acc, x0 + static_cast<uint32_t>(stage) * step_bytes,
+                                                 piece_stride, xo, plain, field, p.m);
+                        cslot = cslot == ring + kAsyncRing - kStageBytes ? ring : cslot + kStageBytes;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(empty(stage));
+                    stage += wk;
+                    if (stage >= stages) {
+                        stage -= stages;
+                        parity ^= 1u;
+                    }
+                }
+            };
+            if (NT == 1 || nt == 1) run(std::integral_constant<int, 1>{});
+            else if (NT == 2 || nt == 2) run(std::integral_constant<int, 2>{});
+            else if (NT == 4 || nt <= 4) run(std::integral_constant<int, 4>{});
+            else run(std::integral_constant<int, 8>{});
+            if (!live) continue;
+            if (plain) F::to_numbers<NT>(acc, field, p.m, t);
+#pragma unroll
+            for (int n0 = 0; n0 < NT; n0 += kJoin) {
+                if (n0 >= nt) break;
+                if (wk == 1) {
+#pragma unroll
+                    for (int n = 0; n < kJoin; ++n)
+                        if (n0 + n < nt) store(tile, n0 + n, lane, make_float4(acc[n0 + n][0], acc[n0 + n][1], acc[n0 + n][2], acc[n0 + n][3]));
+                    continue;
+                }
+#pragma unroll
+                for (int n = 0; n < kJoin; ++n)
+                    area[n * 32 + lane] = make_float4(acc[n0 + n][0], acc[n0 + n][1], acc[n0 + n][2], acc[n0 + n][3]);
+                group_sync(group, wk);
+                for (int i = kw * 32 + lane; i < kJoin * 32; i += wk * 32) {
+                    if (n0 + (i >> 5) >= nt) continue;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int w = 0; w < wk; ++w) {
+                        const float4 q = group_area[w * kAreaVecs + i];
+                        v.x += q.x;
+                        v.y += q.y;
+                        v.z += q.z;
+                        v.w += q.w;
+                    }
+                    store(tile, n0 + (i >> 5), i & 31, v);
+                }
+                group_sync(group, wk);
+            }
+        }
+        cp_async_wait<0>();
+    }
+    if (threadIdx.x == 0)  // every issued copy has landed before the block may exit
+        for (int it = total > stages ? total - stages : 0; it < total; ++it)
+            if (!mbar_wait(full(it % stages), (it / stages) & 1, p.status)) break;
+    __syncwarp();
+    if (S > 1) {
+        cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+        cluster.sync();  // all sums are there
+        const int rows = hi - lo, n = rows * p.m;
+        for (int i = rank * static_cast<int>(blockDim.x) + threadIdx.x; i < n; i += S * static_cast<int>(blockDim.x)) {
+            float s = 0.f;
+            for (int q = 0; q < S; ++q) s += ld_cluster_f32(partial + static_cast<uint32_t>(i) * 4u, static_cast<uint32_t>(q));
+            const int c = i / rows, row = i - c * rows;
+            p.y[static_cast<int64_t>(c) * p.N + lo + row] = static_cast<uint16_t>(pack_bf16x2(s, 0.f));
+        }
+        cluster.sync();  // no block leaves while a peer reads its sums
+    }
+}
+
+// Clusters of S blocks that the device holds at once (asked once per device).
+template <int NT>
+int resident_clusters(cudaLaunchConfig_t& cfg, int S) {
+    static std::atomic<int> known[64][4];
+    const int dev = device_info().device, slot = S == 8 ? 3 : (S == 4 ? 2 : S - 1);
+    int n = known[dev][slot].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (S == 1) n = device_info().sm_count;
+        else if (cudaOccupancyMaxActiveClusters(&n, k_mx4_gemm_async<NT>, &cfg) != cudaSuccess || n < 1) {
+            (void)cudaGetLastError();
+            n = device_info().sm_count / S / 2 > 0 ? device_info().sm_count / S / 2 : 1;
+        }
+        known[dev][slot].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+template <int NT>
+cudaError_t launch_async(AsyncParams p, cudaStream_t stream) {
+    static std::atomic<int> configured[64];
+    cudaError_t e = ensure_dynamic_smem(k_mx4_gemm_async<NT>, kAsyncTotal, configured);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kStreamThreads);
+    cfg.dynamicSmemBytes = kAsyncTotal;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+
+    // S: the one that ends first by a model in cycles of an SM - the copies of X at
+    // some 25 bytes a cycle, the products of a step, the weight at its share of
+    // HBM, and the exchange of sums.
+    const int steps = (p.K + Mx4HalfFmt::kStepCols - 1) / Mx4HalfFmt::kStepCols;
+    const int per_step = NT == 1 ? 50 : (NT == 2 ? 75 : (NT == 4 ? 110 : 200));
+    int64_t best = INT64_MAX;
+    unsigned grid = 1;
+    for (int S = 1; S <= 8 && S <= steps; S *= 2) {
+        cfg.gridDim = dim3(static_cast<unsigned>(S));
+        attr[0].val.clusterDim.x = static_cast<unsigned>(S);
+        cfg.numAttrs = 1;
+        int clusters = resident_clusters<NT>(cfg, S);
+        if (clusters > (p.N + 7) / 8) clusters = (p.N + 7) / 8;
+        const int64_t rows = (p.N + clusters - 1) / clusters;
+        if (S > 1 && (rows + 1) * p.m * 4 > kPartialBytes) continue;
+        const int64_t own = (steps + S - 1) / S, tiles = (rows + 15) / 16;
+        int64_t cost = static_cast<int64_t>(p.m) * own * 256 / 25;
+        if (tiles * own * per_step > cost) cost = tiles * own * per_step;
+        if (rows * own * 3 > cost) cost = rows * own * 3;
+        if (S > 1) cost += 3000;
+        if (cost < best) {
+            best = cost;
+            p.S = S;
+            grid = static_cast<unsigned>(clusters * S);
+        }
+    }
+    cfg.gridDim = dim3(grid);
+    attr[0].val.clusterDim.x = static_cast<unsigned>(p.S);
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_mx4_gemm_async<NT>, p);
+}
+
+cudaError_t launch_prepared(const Mx4View& w, const void* x, void* y, int m, cudaStream_t stream) {
+    const DeviceInfo& dev = device_info();
+    AsyncParams p{};
+    p.w = Mx4HalfFmt::make(w);
+    p.y = static_cast<uint16_t*>(y);
+    p.N = static_cast<int>(w.rows);
+    p.K = static_cast<int>(w.cols);
+    p.m = m;
+    p.status = device_status_ptr();
+    const int steps = (p.K + Mx4HalfFmt::kStepCols - 1) / Mx4HalfFmt::kStepCols;
+    const size_t pieces = static_cast<size_t>(steps) * m * 256;
+    cudaMemPool_t pool;
+    cudaError_t e = scratch_pool(dev.device, &pool);
+    if (e != cudaSuccess) return e;
+    void* ws = nullptr;
+    e = cudaMallocFromPoolAsync(&ws, pieces + kMx4GemmMaxM * 4, pool, stream);
+    if (e != cudaSuccess) return e;
+    uint8_t* xp = static_cast<uint8_t*>(ws);
+    uint32_t* field = reinterpret_cast<uint32_t*>(xp + pieces);
+    p.xp = xp;
+    p.field = field;
+    e = launch_pdl(k_mx4_prepare, dim3(static_cast<unsigned>(m)), dim3(kPrepareThreads), 0, stream, static_cast<const uint16_t*>(x), p.K, m,
+                   steps, xp, field);
+    if (e == cudaSuccess)
+        e = m <= 8 ? launch_async<1>(p, stream)
+                   : (m <= 16 ? launch_async<2>(p, stream) : (m <= 32 ? launch_async<4>(p, stream) : launch_async<8>(p, stream)));
+    const cudaError_t ef = cudaFreeAsync(ws, stream);
+    return e != cudaSuccess ? e : ef;
+}
+
+constexpr int kDirectRows = 4;
+
 }  // namespace
 
 cudaError_t launch_mx4_gemm(const Mx4View& w, const void* x, void* y, int64_t m, cudaStream_t stream) {
     if (w.cols == 0) return cudaMemsetAsync(y, 0, static_cast<size_t>(m * w.rows * 2), stream);  // empty sums
+    if (m > kDirectRows) return launch_prepared(w, x, y, static_cast<int>(m), stream);
     const GemmParams p{Mx4HalfFmt::make(w), static_cast<const uint16_t*>(x), static_cast<uint16_t*>(y), static_cast<int>(w.rows),
                        static_cast<int>(w.cols), static_cast<int>(m)};
-    if (m <= 8) return launch_nt<1>(p, stream);
-    if (m <= 16) return launch_nt<2>(p, stream);
-    if (m <= 32) return launch_nt<4>(p, stream);
-    return launch_nt<8>(p, stream);
+    return launch_nt<1>(p, stream);
 }
 
 }  // namespace mlxq

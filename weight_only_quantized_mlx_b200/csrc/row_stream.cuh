@@ -476,12 +476,19 @@ __device__ __forceinline__ uint32_t scaled_half2(uint32_t bf16x2, float f) {
 // Stage the activations of `cols` columns for steps [s0, s0 + n): piece (step,
 // i, column, t) of 16 bytes at ((step kPieces + i) cols + column) 64 + 16 t.
 // row(c): column c's activations (K of them; zeros behind).  All threads of the
-// block; the caller synchronises before (the buffer is free) and after.
+// block; the caller synchronises before (the buffer is free) and after.  A warp
+// takes 32 consecutive pieces of a column at a time, four such lots in flight;
+// the blocks begin at different lots, since a line that all of them want at once
+// is served to one after another.
 template <class F, class Row>
 __device__ __forceinline__ void stage_columns(const XBuffer& xb, int cols, int s0, int n, int K, Row row) {
     constexpr int kPer = 4 * F::kPieces;  // pieces of a column and step
-    const int per_col = n * kPer, all = cols * per_col;
+    constexpr int kLots = 4;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per_col = n * kPer, lots = (per_col + 31) >> 5, all = cols * lots;
+    const int first = static_cast<int>(static_cast<int64_t>(all) * blockIdx.x / gridDim.x);
     const int k0 = s0 * F::kStepCols;
+    const uint32_t stride = static_cast<uint32_t>(cols) * 64u;
     if (F::kScaled) {
         for (int c = threadIdx.x; c < cols; c += kStreamThreads) {
             const uint32_t f = s0 == 0 ? 0u : xb.field[c];
@@ -490,29 +497,49 @@ __device__ __forceinline__ void stage_columns(const XBuffer& xb, int cols, int s
         }
         __syncthreads();
     }
-    auto place = [&](int i, int& c) {
-        c = i / per_col;
-        const int q = i - c * per_col, step = q / kPer, r = q % kPer;
-        return xb.addr + static_cast<uint32_t>((step * F::kPieces + F::piece_index(r)) * cols + c) * 64u + F::piece_lane(r) * 16u;
+    auto place = [&](int c, int q) {
+        const int step = q / kPer, r = q % kPer;
+        return xb.addr + static_cast<uint32_t>(step * F::kPieces + F::piece_index(r)) * stride + static_cast<uint32_t>(c) * 64u +
+               F::piece_lane(r) * 16u;
     };
-#pragma unroll 8
-    for (int i = threadIdx.x; i < all; i += kStreamThreads) {
-        int c;
-        const uint32_t at = place(i, c);
-        const int k = k0 + 8 * (i - c * per_col);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (k < K) v = ldg128(row(c) + k);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-        if (F::kScaled) {
-            const uint32_t f = max_field(v);
-            if (f > 0) atomicMax(xb.field + c, f);
+    for (int u0 = warp; u0 < all; u0 += kStreamWarps * kLots) {
+        uint4 v[kLots];
+        uint32_t at[kLots];
+        int col[kLots];
+#pragma unroll
+        for (int j = 0; j < kLots; ++j) {
+            int u = u0 + j * kStreamWarps;
+            v[j] = make_uint4(0u, 0u, 0u, 0u);
+            col[j] = -1;
+            if (u < all) {
+                u += first;
+                if (u >= all) u -= all;
+                const int c = u / lots, q = (u - c * lots) * 32 + lane;
+                if (q < per_col) {
+                    col[j] = c;
+                    at[j] = place(c, q);
+                    if (k0 + 8 * q < K) v[j] = ldg128(row(c) + k0 + 8 * q);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kLots; ++j) {
+            if (col[j] >= 0)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at[j]), "r"(v[j].x), "r"(v[j].y), "r"(v[j].z), "r"(v[j].w)
+                             : "memory");
+            if (F::kScaled) {
+                const uint32_t f = __reduce_max_sync(0xFFFFFFFFu, max_field(v[j]));
+                if (lane == 0 && f > 0) atomicMax(xb.field + col[j], f);  // f > 0: the lot has pieces, lane 0 one of them
+            }
         }
     }
     if (F::kScaled) {
         __syncthreads();
-        for (int i = threadIdx.x; i < all; i += kStreamThreads) {  // the pieces this thread wrote
-            int c;
-            const uint32_t at = place(i, c);
+        for (int u1 = warp; u1 < all; u1 += kStreamWarps) {  // the pieces this thread wrote
+            const int u = u1 + first < all ? u1 + first : u1 + first - all;
+            const int c = u / lots, q = (u - c * lots) * 32 + lane;
+            if (q >= per_col) continue;
+            const uint32_t at = place(c, q);
             const float f = __uint_as_float((254u - x_field(xb.field[c])) << 23);  // 1 / unit
             const uint4 v = lds128(at);
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(scaled_half2(v.x, f)), "r"(scaled_half2(v.y, f)),
