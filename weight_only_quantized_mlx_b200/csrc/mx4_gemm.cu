@@ -4,7 +4,7 @@
 // ranges of its rows, every byte once (row_stream.cuh).  One rounding, of the
 // result.
 //
-// k_mx4_gemm, up to kDirectRows rows of X: a block keeps them in shared memory,
+// k_mx4_gemm, up to 8 rows of X: a block keeps them in shared memory,
 // converted on the way (in chunks of K where they do not fit).
 //
 // k_mx4_gemm_async, more rows: every block needs all of X over its columns, and
@@ -100,14 +100,21 @@ struct AsyncParams {
     unsigned int* status;
 };
 
-constexpr int kAsyncDepth = 4;  // ring stages of a warp: with X in a ring beside them, six leave too little room for it
-constexpr uint32_t kAsyncRing = kAsyncDepth * kStageBytes;
-constexpr uint32_t kAsyncAreas = kStreamWarps * kAsyncRing;
-constexpr uint32_t kAsyncFields = kAsyncAreas + kStreamWarps * kSharedArea;
-constexpr uint32_t kAsyncX = kAsyncFields + kMx4GemmMaxM * 4;
 constexpr uint32_t kPartialBytes = 32 * 1024;  // S > 1: fp32 sums of a cluster's rows
 constexpr int kMaxXStages = 16;
 constexpr uint32_t kAsyncTotal = 227 * 1024 - 512;
+
+// Shared memory: weight rings | areas | units | sums (S > 1) | steps of X.  Four
+// stages a warp's ring (six measured no faster, and take the room of steps of X).
+template <int NT>
+struct AsyncSmem {
+    static constexpr int kDepth = 4;
+    static constexpr uint32_t kRing = kDepth * kStageBytes;
+    static constexpr uint32_t kAreas = kStreamWarps * kRing;
+    static constexpr uint32_t kFields = kAreas + kStreamWarps * kSharedArea;
+    static constexpr uint32_t kX = kFields + kMx4GemmMaxM * 4;
+    static_assert(kAsyncTotal - kX - kPartialBytes >= 2u * NT * 8 * 256, "two steps of X");
+};
 
 // A block per row of X: its unit (the largest exponent), then its pieces.
 constexpr int kPrepareThreads = 512;
@@ -146,6 +153,7 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
 template <int NT>
 __global__ void __launch_bounds__(kStreamThreads, 1) k_mx4_gemm_async(const __grid_constant__ AsyncParams p) {
     using F = Mx4HalfFmt;
+    using M = AsyncSmem<NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[2 * kMaxXStages];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -159,9 +167,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_mx4_gemm_async(const __gr
     const int steps = static_cast<int>(static_cast<int64_t>(all_steps) * (rank + 1) / S) - st0;
     const int tiles = (hi - lo + 15) / 16;
     const uint32_t step_bytes = static_cast<uint32_t>(p.m) * 256u;
-    const uint32_t partial = smem_u32(smem) + kAsyncX, x0 = partial + (S > 1 ? kPartialBytes : 0u);
+    const uint32_t partial = smem_u32(smem) + M::kX, x0 = partial + (S > 1 ? kPartialBytes : 0u);
     const int room = min(static_cast<int>((smem_u32(smem) + kAsyncTotal - x0) / step_bytes), kMaxXStages);
-    uint32_t* field = reinterpret_cast<uint32_t*>(smem + kAsyncFields);
+    uint32_t* field = reinterpret_cast<uint32_t*>(smem + M::kFields);
 
     // Warps per tile (lane i weighs 2^i of them): steps, and two for a join.  A
     // stage of X is one step; their number is a multiple of the warps of a tile,
@@ -202,9 +210,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_mx4_gemm_async(const __gr
     __syncwarp();
     {
         const int group = warp >> lw, kw = warp & (wk - 1);
-        const uint32_t ring = smem_u32(smem) + warp * kAsyncRing;
-        float4* area = reinterpret_cast<float4*>(smem + kAsyncAreas + warp * kSharedArea);
-        const float4* group_area = reinterpret_cast<const float4*>(smem + kAsyncAreas + group * wk * kSharedArea);
+        const uint32_t ring = smem_u32(smem) + warp * M::kRing;
+        float4* area = reinterpret_cast<float4*>(smem + M::kAreas + warp * kSharedArea);
+        const float4* group_area = reinterpret_cast<const float4*>(smem + M::kAreas + group * wk * kSharedArea);
         constexpr int kAreaVecs = kSharedArea / 16;
         constexpr int kJoin = NT < 4 ? NT : 4;  // column tiles of a join
 
@@ -230,10 +238,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_mx4_gemm_async(const __gr
                 }
             }
             cp_async_commit();
-            pslot = pslot == ring + kAsyncRing - kStageBytes ? ring : pslot + kStageBytes;
+            pslot = pslot == ring + M::kRing - kStageBytes ? ring : pslot + kStageBytes;
         };
 #pragma unroll 1
-        for (int i = 0; i < kAsyncDepth - 1; ++i) issue();
+        for (int i = 0; i < M::kDepth - 1; ++i) issue();
         for (int c = threadIdx.x; c < p.m; c += kStreamThreads) field[c] = p.field[c];
         __syncthreads();  // the fields are there
 
@@ -285,12 +293,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_mx4_gemm_async(const __gr
                     // after a wait has given up there are no more, the control flow goes on
                     if (ok) ok = mbar_wait(full(stage), parity, p.status);
                     if (live && k < steps) {
-                        cp_async_wait<kAsyncDepth - 2>();
+                        cp_async_wait<M::kDepth - 2>();
                         __syncwarp();  // the copies of all lanes have landed; the slot refilled below is read out
                         issue();
                         F::consume_shared<NT, N>(p.w, cslot, lane, key, st0 + k, acc, x0 + static_cast<uint32_t>(stage) * step_bytes,
                                                  piece_stride, xo, plain, field, p.m);
-                        cslot = cslot == ring + kAsyncRing - kStageBytes ? ring : cslot + kStageBytes;
+                        cslot = cslot == ring + M::kRing - kStageBytes ? ring : cslot + kStageBytes;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(empty(stage));
@@ -451,13 +459,18 @@ cudaError_t launch_prepared(const Mx4View& w, const void* x, void* y, int m, cud
     return e != cudaSuccess ? e : ef;
 }
 
-constexpr int kDirectRows = 4;
+// Preparing costs a launch and a pass over X, about 4 us; without it a block
+// refills its copy of X for every round of tiles.  Measured at 8 rows: 10.7
+// against 12.0 us at 4096 x 4096 and 48 against 54 at 28672 x 8192 without it, but
+// 72 against 54 at 8192 x 28672; at 16 rows 18 against 13 and 74 against 67.
+constexpr int kDirectRows = 8;
+constexpr int64_t kDirectBytes = 160 * 1024;
 
 }  // namespace
 
 cudaError_t launch_mx4_gemm(const Mx4View& w, const void* x, void* y, int64_t m, cudaStream_t stream) {
     if (w.cols == 0) return cudaMemsetAsync(y, 0, static_cast<size_t>(m * w.rows * 2), stream);  // empty sums
-    if (m > kDirectRows) return launch_prepared(w, x, y, static_cast<int>(m), stream);
+    if (m > kDirectRows || m * w.cols * 2 > kDirectBytes) return launch_prepared(w, x, y, static_cast<int>(m), stream);
     const GemmParams p{Mx4HalfFmt::make(w), static_cast<const uint16_t*>(x), static_cast<uint16_t*>(y), static_cast<int>(w.rows),
                        static_cast<int>(w.cols), static_cast<int>(m)};
     return launch_nt<1>(p, stream);

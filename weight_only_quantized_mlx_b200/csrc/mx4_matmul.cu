@@ -8,8 +8,9 @@
 //   warp 0      TMA: the codes of both operands (128-byte swizzle)
 //   warp 1      allocates TMEM; one lane copies each k-block's scales into TMEM
 //               (tcgen05.cp) and issues the MMAs
-//   warps 2, 3  scales of the weight rows and of the activation rows: 8 bytes a
-//               row and k-block, put into the 128 x 4 order that tcgen05.cp and
+//   warps 2, 3 and 12, 13  scales of the weight rows and of the activation rows,
+//               128 rows each: 8 bytes a row and k-block, loaded two k-blocks
+//               ahead, put into the 128 x 4 order that tcgen05.cp and
 //               the MMA expect (row r, group g of a set of four: byte
 //               (r % 32) 16 + (r / 32) 4 + g)
 //   warps 4-11  read the accumulators (tcgen05.ld) as BF16 into registers,
@@ -42,7 +43,8 @@ constexpr uint32_t kStageX = kMaxBN * 128;   // codes of the activation rows
 constexpr uint32_t kStageS = 2048;           // scales of one operand: [half][set][32][16]
 constexpr uint32_t kStageBytes = kStageW + kStageX + 2 * kStageS;
 constexpr int kFirstEpilogue = 4;
-constexpr int kThreads = (kFirstEpilogue + 8) * 32;
+constexpr int kFirstXScales = kFirstEpilogue + 8;
+constexpr int kThreads = (kFirstXScales + 2) * 32;
 constexpr uint32_t kAccCols = kMaxBN;        // TMEM columns of one half's sums
 constexpr uint32_t kScaleCol = 2 * kAccCols; // then two buffers of 32 columns of scales
 static_assert(kScaleCol + 2 * 32 <= 512, "TMEM columns");
@@ -53,7 +55,6 @@ struct MatmulParams {
     const uint8_t* a_scales;
     int N, m, G;        // weight rows, activation rows, scale bytes per row
     int BN, num_kb;
-    int scale_load;     // bytes per load of scales: 8, 4 or 1
     uint32_t idesc;
     unsigned int* status;
 };
@@ -97,24 +98,56 @@ __device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
            static_cast<uint64_t>(128u >> 4) << 32 | static_cast<uint64_t>(1u) << 46;
 }
 
-// The eight scale bytes of one row and k-block; 127 (scale 1) where there is none.
-__device__ __forceinline__ uint2 load_scales(const uint8_t* row, bool live, int g0, int G, int bytes) {
-    uint2 v = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    if (!live) return v;
-    if (bytes == 8) return __ldg(reinterpret_cast<const uint2*>(row + g0));
-    if (bytes == 4) {
-        v.x = __ldg(reinterpret_cast<const uint32_t*>(row + g0));
-        if (g0 + 4 < G) v.y = __ldg(reinterpret_cast<const uint32_t*>(row + g0 + 4));
-        return v;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (g0 + i < G) v.x = (v.x & ~(0xFFu << (8 * i))) | static_cast<uint32_t>(__ldg(row + g0 + i)) << (8 * i);
-        if (g0 + 4 + i < G) v.y = (v.y & ~(0xFFu << (8 * i))) | static_cast<uint32_t>(__ldg(row + g0 + 4 + i)) << (8 * i);
-    }
+// The eight scale bytes of one row and k-block, from the table's byte e on: words
+// now, bytes when they are due, so that the loads of many rows are in flight
+// together.  WIDE: rows are multiples of 8 bytes and the table is 8-byte aligned.
+// Otherwise the bytes start anywhere in a word; words that the table does not
+// have all of are not read.
+__device__ __forceinline__ uint32_t ldg_if(const uint8_t* p, bool read) {
+    uint32_t v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "mov.u32 %0, 0;\n\t"
+        "@p ld.global.nc.u32 %0, [%1];\n\t}"
+        : "=r"(v)
+        : "l"(p), "r"(static_cast<uint32_t>(read)));
     return v;
 }
+template <bool WIDE>
+__device__ __forceinline__ void load_words(uint32_t (&w)[WIDE ? 2 : 3], const uint8_t* scales, int64_t e, int64_t table, bool live) {
+    if (WIDE) {
+        uint2 v = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        if (live) v = __ldg(reinterpret_cast<const uint2*>(scales + e));
+        w[0] = v.x;
+        w[1] = v.y;
+        return;
+    }
+    const int64_t at = e & ~int64_t{3};
+#pragma unroll
+    for (int i = 0; i < 3; ++i) w[i] = ldg_if(scales + at + 4 * i, live && at + 4 * i + 4 <= table);
+}
+// `left`: blocks left in the row; behind them, and where there is no row, 127 (scale 1).
+template <bool WIDE>
+__device__ __forceinline__ uint2 scale_bytes(const uint32_t (&w)[WIDE ? 2 : 3], const uint8_t* scales, int64_t e, int64_t table, bool live,
+                                             int left) {
+    if (WIDE) return make_uint2(w[0], w[1]);
+    if (!live) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    const uint32_t sh = 8u * static_cast<uint32_t>(e & 3);
+    uint32_t lo = __funnelshift_r(w[0], w[1], sh), hi = __funnelshift_r(w[1], w[WIDE ? 1 : 2], sh);
+    if (e + 8 > (table & ~int64_t{3})) {  // the table's last bytes, not a whole word
+        lo = hi = 0;
+        for (int i = 0; i < 4; ++i) {
+            if (e + i < table) lo |= static_cast<uint32_t>(__ldg(scales + e + i)) << (8 * i);
+            if (e + 4 + i < table) hi |= static_cast<uint32_t>(__ldg(scales + e + 4 + i)) << (8 * i);
+        }
+    }
+    const uint32_t k0 = left >= 4 ? 0xFFFFFFFFu : (1u << (8 * left)) - 1u;
+    const uint32_t k1 = left >= 8 ? 0xFFFFFFFFu : (left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u);
+    return make_uint2((lo & k0) | (0x7F7F7F7Fu & ~k0), (hi & k1) | (0x7F7F7F7Fu & ~k1));
+}
 
+template <bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_mx4_matmul(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const MatmulParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -139,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(sfull(s), 2);
+            mbar_init(sfull(s), 4);
             mbar_init(empty(s), 1);
         }
         mbar_init(acc_full, 1);
@@ -225,47 +258,61 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait(drain, 0, p.status);
         }
         __syncwarp();
-    } else if (warp < kFirstEpilogue) {
+    } else if (warp < kFirstEpilogue || warp >= kFirstXScales) {
         // ---------------- scales ----------------
-        const bool weight = warp == 2;
+        const bool weight = warp < kFirstEpilogue;
+        const int half = warp & 1;  // rows 128 half ..
         const uint8_t* scales = weight ? p.w_scales : p.a_scales;
         const int rows = weight ? p.N : p.m, span = weight ? kBM : p.BN;
-        uint2 v[8];
-        auto load = [&](int tile, int kb) {
-            const int r0 = weight ? (tile % tiles_n) * kBM : (tile / tiles_n) * p.BN;
+        const int64_t table = static_cast<int64_t>(rows) * p.G;
+        constexpr int kWords = WIDE ? 2 : 3;
+        auto first_row = [&](int tile) { return weight ? (tile % tiles_n) * kBM : (tile / tiles_n) * p.BN; };
+        auto load = [&](uint32_t (&v)[4][kWords], int tile, int kb) {
+            const int r0 = first_row(tile);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = lane + 32 * i;
-                v[i] = load_scales(scales + static_cast<int64_t>(r0 + r) * p.G, r < span && r0 + r < rows, kb * 8, p.G, p.scale_load);
+            for (int i = 0; i < 4; ++i) {
+                const int r = half * 128 + lane + 32 * i;
+                load_words<WIDE>(v[i], scales, static_cast<int64_t>(r0 + r) * p.G + kb * 8, table, r < span && r0 + r < rows);
             }
         };
         bool ok = true;
-        int it = 0;
-        if (static_cast<int>(blockIdx.x) < tiles) load(blockIdx.x, 0);
+        int it = 0, ltile = blockIdx.x, lkb = 0;  // what is loaded next
+        uint32_t v[2][4][kWords];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (ltile < tiles) load(v[i], ltile, lkb);
+            if (++lkb == num_kb) {
+                lkb = 0;
+                ltile += gridDim.x;
+            }
+        }
         for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            const int r0 = first_row(tile);
             for (int kb = 0; kb < num_kb; ++kb, ++it) {
                 const int s = it % kStages;
-                uint2 c[8];
+                uint2 c[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) c[i] = v[i];
-                // the next k-block's loads are in flight while this one waits for its stage
-                if (kb + 1 < num_kb) load(tile, kb + 1);
-                else if (tile + static_cast<int>(gridDim.x) < tiles) load(tile + gridDim.x, 0);
+                for (int i = 0; i < 4; ++i) {
+                    const int r = half * 128 + lane + 32 * i;
+                    c[i] = scale_bytes<WIDE>(v[0][i], scales, static_cast<int64_t>(r0 + r) * p.G + kb * 8, table, r < span && r0 + r < rows,
+                                             p.G - kb * 8);
+#pragma unroll
+                    for (int j = 0; j < kWords; ++j) v[0][i][j] = v[1][i][j];
+                }
+                if (ltile < tiles) load(v[1], ltile, lkb);
+                if (++lkb == num_kb) {
+                    lkb = 0;
+                    ltile += gridDim.x;
+                }
                 if (it >= kStages) ok = mbar_wait(empty(s), ((it / kStages) - 1) & 1, p.status);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
                 }
-                const uint32_t dst = (weight ? SW_of(s) : SX_of(s)) + static_cast<uint32_t>(lane) * 16u;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 1024u * h), "r"(c[4 * h].x), "r"(c[4 * h + 1].x),
-                                 "r"(c[4 * h + 2].x), "r"(c[4 * h + 3].x)
-                                 : "memory");
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 1024u * h + 512u), "r"(c[4 * h].y),
-                                 "r"(c[4 * h + 1].y), "r"(c[4 * h + 2].y), "r"(c[4 * h + 3].y)
-                                 : "memory");
-                }
+                const uint32_t dst = (weight ? SW_of(s) : SX_of(s)) + 1024u * half + static_cast<uint32_t>(lane) * 16u;
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(c[0].x), "r"(c[1].x), "r"(c[2].x), "r"(c[3].x) : "memory");
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 512u), "r"(c[0].y), "r"(c[1].y), "r"(c[2].y), "r"(c[3].y)
+                             : "memory");
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sfull(s));
@@ -329,14 +376,19 @@ int pick_bn(int64_t m, int64_t N, int sms) {
     return best;
 }
 
+template <bool WIDE>
+cudaError_t launch(unsigned grid, const CUtensorMap& tm_w, const CUtensorMap& tm_a, const MatmulParams& p, cudaStream_t stream) {
+    static std::atomic<int> configured[64];
+    const size_t smem = kStages * kStageBytes + 1024;
+    cudaError_t e = ensure_dynamic_smem(k_mx4_matmul<WIDE>, smem, configured);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_mx4_matmul<WIDE>, dim3(grid), dim3(kThreads), smem, stream, tm_w, tm_a, p);
+}
+
 }  // namespace
 
 cudaError_t launch_mx4_matmul(const Mx4View& w, const Mx4View& a, void* y, cudaStream_t stream) {
     if (w.cols == 0) return cudaMemsetAsync(y, 0, static_cast<size_t>(a.rows * w.rows * 2), stream);  // empty sums
-    static std::atomic<int> configured[64];
-    const size_t smem = kStages * kStageBytes + 1024;
-    cudaError_t e = ensure_dynamic_smem(k_mx4_matmul, smem, configured);
-    if (e != cudaSuccess) return e;
     const int sms = device_info().sm_count;
     MatmulParams p{};
     p.Y = static_cast<uint16_t*>(y);
@@ -348,7 +400,7 @@ cudaError_t launch_mx4_matmul(const Mx4View& w, const Mx4View& a, void* y, cudaS
     p.BN = pick_bn(a.rows, w.rows, sms);
     p.num_kb = static_cast<int>((w.cols + kBK - 1) / kBK);
     const bool a8 = ((reinterpret_cast<uintptr_t>(w.scales) | reinterpret_cast<uintptr_t>(a.scales)) & 7u) == 0;
-    p.scale_load = p.G % 8 == 0 && a8 ? 8 : (p.G % 4 == 0 ? 4 : 1);
+    const bool wide = p.G % 8 == 0 && a8;
     // kind::mxf4: A and B E2M1 (1), scales UE8M0 (bit 23), N / 8, M / 128
     p.idesc = 1u << 7 | 1u << 10 | static_cast<uint32_t>(p.BN / 8) << 17 | 1u << 23 | 1u << 27;
     p.status = device_status_ptr();
@@ -360,7 +412,8 @@ cudaError_t launch_mx4_matmul(const Mx4View& w, const Mx4View& a, void* y, cudaS
         return cudaErrorInvalidValue;
     const int64_t tiles = ((w.rows + kBM - 1) / kBM) * ((a.rows + p.BN - 1) / p.BN);
     if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;
-    return launch_pdl(k_mx4_matmul, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kThreads), smem, stream, tm_w, tm_a, p);
+    const unsigned grid = static_cast<unsigned>(tiles < sms ? tiles : sms);
+    return wide ? launch<true>(grid, tm_w, tm_a, p, stream) : launch<false>(grid, tm_w, tm_a, p, stream);
 }
 
 }  // namespace mlxq
