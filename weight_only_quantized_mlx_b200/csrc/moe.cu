@@ -31,7 +31,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kMaxExperts = kMoeMaxExperts;
 constexpr int kRouterCluster = 8;
-constexpr int kRouterWarps = 8;
+constexpr int kRouterWarps = 16;
 
 // Workspace (see moe_workspace_bytes): 256 bytes holding the barrier count,
 // ids [slots], shares [slots], h [slots][inter].
@@ -93,7 +93,7 @@ __global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(kRouter
     pdl_wait();
     // experts rank, rank + 8, ...; with fewer of them than warps, several warps share one's H
     const int mine = p.E > rank ? (p.E - rank - 1) / kRouterCluster + 1 : 0;
-    const int split = mine > 4 ? 1 : (mine > 2 ? 2 : (mine > 1 ? 4 : 8));
+    const int split = mine > 8 ? 1 : (mine > 4 ? 2 : (mine > 2 ? 4 : (mine > 1 ? 8 : 16)));
     const int sub = warp % split, chunks = p.H / 8;
     for (int i = warp / split; i < mine; i += kRouterWarps / split) {
         const uint4* r = reinterpret_cast<const uint4*>(p.router + static_cast<int64_t>(rank + kRouterCluster * i) * p.H);
@@ -196,8 +196,13 @@ struct ExpertLists {
     int16_t off[kMaxEntries];    // its first column
     int16_t cnt[kMaxEntries];    // its columns
     int16_t cols[kMaxListed];    // slots
+    long long before[kMaxEntries + 1];  // NT > 1: weight of all gate and up rows before entry a's
     int entries;
     int stop;
+
+    // What a row of entry a costs: some fixed work, and the products of its column
+    // tiles (measured 132, 165 and 243 cycles a step at one, two and four).
+    __device__ __forceinline__ int weight(int a) const { return cnt[a] <= 8 ? 4 : (cnt[a] <= 16 ? 5 : 7); }
 };
 
 struct Columns {
@@ -212,12 +217,15 @@ struct Columns {
 // order of an entry's columns has no effect on results (MMA columns are
 // independent), so they are placed by atomics; which entry of several a token
 // falls into could change the order of sums, so there a slot's place is its rank.
-template <int NT>
-__device__ __forceinline__ void build_lists(ExpertLists& L, const int* ids, int slots, int top_k, int E) {
-    const int tid = threadIdx.x, lane = tid & 31;
-    for (int e = tid; e < E; e += kStreamThreads) L.count[e] = 0;
-    for (int c = tid; c < kMaxListed; c += kStreamThreads) L.cols[c] = -1;
+__device__ __forceinline__ void clear_lists(ExpertLists& L, int E) {
+    for (int e = threadIdx.x; e < E; e += kStreamThreads) L.count[e] = 0;
+    for (int c = threadIdx.x; c < kMaxListed; c += kStreamThreads) L.cols[c] = -1;
     __syncthreads();
+}
+
+template <int NT>
+__device__ __forceinline__ void build_lists(ExpertLists& L, const int* ids, int slots, int top_k, int E, int I) {
+    const int tid = threadIdx.x, lane = tid & 31;
     for (int s = tid; s < slots; s += kStreamThreads) atomicAdd(&L.count[ids[s]], 1);
     __syncthreads();
     if (tid < 32) {  // exclusive sums over the experts: first entry and first column
@@ -259,6 +267,21 @@ __device__ __forceinline__ void build_lists(ExpertLists& L, const int* ids, int 
         }
         L.cols[c] = static_cast<int16_t>(s);
     }
+    if (NT > 1 && tid < 32) {  // exclusive sums of the entries' weights
+        long long sum = 0;
+        for (int a0 = 0; a0 < L.entries; a0 += 32) {
+            const int a = a0 + lane;
+            long long v = a < L.entries ? static_cast<long long>(I) * L.weight(a) : 0;
+            const long long mine = v;
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long u = __shfl_up_sync(0xFFFFFFFFu, v, d);
+                if (lane >= d) v += u;
+            }
+            if (a < L.entries) L.before[a] = sum + v - mine;
+            sum += __shfl_sync(0xFFFFFFFFu, v, 31);
+        }
+        if (lane == 0) L.before[L.entries] = sum;
+    }
     __syncthreads();
 }
 
@@ -295,7 +318,7 @@ template <int NT>
 struct Smem {
     static constexpr int kTokens = NT == 1 ? 8 : (NT == 2 ? 16 : kMoeMaxTokens);  // most tokens of a call
     static constexpr uint32_t kDownArea = NT == 1 ? 2048 : 16 * (kTokens + 4) * 4;  // a warp's sums of the down phase
-    static constexpr uint32_t kLists = kStreamWarps * kRingBytes;
+    static constexpr uint32_t kLists = kStreamWarps * Ring<NT>::kBytes;
     static constexpr uint32_t kAreas = (kLists + sizeof(ExpertLists) + 127) / 128 * 128;
     static constexpr uint32_t kFields = kAreas + kStreamWarps * kSharedArea;
     static constexpr uint32_t kX = kFields + 2 * kMoeMaxTokens * 4;
@@ -321,15 +344,27 @@ struct GateUpJob {
 
     __device__ __forceinline__ GateUpJob(const ExpertParams<F>& p_, const ExpertLists& L_, const Columns& cm_)
         : p(p_), mat(p_.gate), L(L_), cm(cm_) {
-        const int64_t rows = static_cast<int64_t>(L.entries) * p.I;
-        lo = rows * blockIdx.x / gridDim.x;
-        hi = rows * (blockIdx.x + 1) / gridDim.x;
+        lo = first_row(blockIdx.x);
+        hi = first_row(blockIdx.x + 1);
         K = p.H;
         per = p.I >> 3;
         o0 = static_cast<int>(lo >> 3);
         octets = lo < hi ? static_cast<int>((hi - 1) >> 3) - o0 + 1 : 0;
         a_first = o0 / per;
         segs = octets == 0 ? 0 : (NT == 1 ? 1 : (o0 + octets - 1) / per - a_first + 1);
+    }
+    // The first of the rows that block b takes: shares of equal weight.
+    __device__ __forceinline__ int64_t first_row(unsigned b) const {
+        if (NT == 1) return static_cast<int64_t>(L.entries) * p.I * b / gridDim.x;
+        const long long at = L.before[L.entries] * b / gridDim.x;
+        int a = 0, n = L.entries;  // the last entry that begins at or before `at`
+        while (n > 1) {
+            const int half = n >> 1;
+            if (L.before[a + half] <= at) a += half;
+            n -= half;
+        }
+        const int64_t row = static_cast<int64_t>(a) * p.I + (at - L.before[a]) / L.weight(a);
+        return row;
     }
     __device__ __forceinline__ int begin(int s) const { return NT == 1 ? 0 : max((a_first + s) * per - o0, 0); }
     __device__ __forceinline__ int end(int s) const { return NT == 1 ? octets : min((a_first + s + 1) * per - o0, octets); }
@@ -380,6 +415,8 @@ struct GateUpJob {
 template <class F, int NT, class Params, class Ready>
 __device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L, const Columns& cm, uint32_t ring,
                                            uint8_t* areas, Ready ready) {
+    constexpr int kDepth = Ring<NT>::kDepth;
+    constexpr uint32_t kRingBytes = Ring<NT>::kBytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int lo = static_cast<int>(static_cast<int64_t>(p.H) * blockIdx.x / gridDim.x);
     const int hi = static_cast<int>(static_cast<int64_t>(p.H) * (blockIdx.x + 1) / gridDim.x);
@@ -578,9 +615,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_moe_experts(const __grid_
     using M = Smem<NT>;
     ExpertLists& L = *reinterpret_cast<ExpertLists*>(smem + M::kLists);
     uint32_t* field = reinterpret_cast<uint32_t*>(smem + M::kFields);
-    const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * kRingBytes;
+    const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * Ring<NT>::kBytes;
+    clear_lists(L, p.E);
     pdl_wait();
-    build_lists<NT>(L, p.ws.ids, p.m * p.top_k, p.top_k, p.E);
+    build_lists<NT>(L, p.ws.ids, p.m * p.top_k, p.top_k, p.E, p.I);
     const Columns cm{L.cols, L.off, L.cnt, p.top_k};
     const XBuffer xb{smem_u32(smem) + M::kX, static_cast<int>(M::kXBytes), field, field + kMoeMaxTokens};
     shared_phase<FG, NT>(GateUpJob<FG, NT>(p, L, cm), ring, smem + M::kAreas, xb);
@@ -604,11 +642,13 @@ cudaError_t launch_experts(const ExpertParams<FG>& p, cudaStream_t stream) {
     cfg.blockDim = dim3(kStreamThreads);
     cfg.dynamicSmemBytes = Smem<NT>::kTotal;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;  // the grid barrier needs every block resident
     attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, k_moe_experts<FG, FD, NT>, p);
 }
 

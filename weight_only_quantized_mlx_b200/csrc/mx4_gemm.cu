@@ -65,29 +65,27 @@ struct GemmJob {
     }
 };
 
-constexpr uint32_t kAreas = kStreamWarps * kRingBytes;
+constexpr uint32_t kAreas = kStreamWarps * Ring<1>::kBytes;
 constexpr uint32_t kFields = kAreas + kStreamWarps * kSharedArea;
 constexpr uint32_t kX = kFields + 2 * kMx4GemmMaxM * 4;
 constexpr uint32_t kTotal = 227 * 1024;
 
-template <int NT>
 __global__ void __launch_bounds__(kStreamThreads, 1) k_mx4_gemm(const __grid_constant__ GemmParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
     pdl_launch_dependents();
     uint32_t* field = reinterpret_cast<uint32_t*>(smem + kFields);
-    const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * kRingBytes;
+    const uint32_t ring = smem_u32(smem) + (threadIdx.x >> 5) * Ring<1>::kBytes;
     const XBuffer xb{smem_u32(smem) + kX, static_cast<int>(kTotal - kX), field, field + kMx4GemmMaxM};
     pdl_wait();
-    shared_phase<Mx4HalfFmt, NT>(GemmJob(p), ring, smem + kAreas, xb);
+    shared_phase<Mx4HalfFmt, 1>(GemmJob(p), ring, smem + kAreas, xb);
 }
 
-template <int NT>
-cudaError_t launch_nt(const GemmParams& p, cudaStream_t stream) {
+cudaError_t launch_direct(const GemmParams& p, cudaStream_t stream) {
     static std::atomic<int> configured[64];
-    cudaError_t e = ensure_dynamic_smem(k_mx4_gemm<NT>, kTotal, configured);
+    cudaError_t e = ensure_dynamic_smem(k_mx4_gemm, kTotal, configured);
     if (e != cudaSuccess) return e;
     const int sms = device_info().sm_count, octets = (p.N + 7) / 8;
-    return launch_pdl(k_mx4_gemm<NT>, dim3(static_cast<unsigned>(octets < sms ? octets : sms)), dim3(kStreamThreads), kTotal, stream, p);
+    return launch_pdl(k_mx4_gemm, dim3(static_cast<unsigned>(octets < sms ? octets : sms)), dim3(kStreamThreads), kTotal, stream, p);
 }
 
 // ---- more rows ------------------------------------------------------------------------------
@@ -473,7 +471,7 @@ cudaError_t launch_mx4_gemm(const Mx4View& w, const void* x, void* y, int64_t m,
     if (m > kDirectRows || m * w.cols * 2 > kDirectBytes) return launch_prepared(w, x, y, static_cast<int>(m), stream);
     const GemmParams p{Mx4HalfFmt::make(w), static_cast<const uint16_t*>(x), static_cast<uint16_t*>(y), static_cast<int>(w.rows),
                        static_cast<int>(w.cols), static_cast<int>(m)};
-    return launch_nt<1>(p, stream);
+    return launch_direct(p, stream);
 }
 
 }  // namespace mlxq

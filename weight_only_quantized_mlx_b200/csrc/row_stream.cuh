@@ -6,7 +6,7 @@
 // A warp works on tiles of 16 weight rows (two halves of 8: rows g of half A
 // and half B belong to lanes 4g .. 4g + 3) and walks K in steps of 64 bytes of
 // codes per row.  Lane (g, t) copies bytes 16t .. 16t + 15 of the step in its
-// two rows with cp.async into the warp's own ring in shared memory (kDepth steps
+// two rows with cp.async into the warp's own ring in shared memory (several steps
 // in flight per warp, no block barrier).  The codes become 16-bit operands in
 // registers and go to mma.sync m16n8k16 as A, with the activations (8 columns
 // per MMA) as B.  A sum over k may be taken in any order, so each MMA's k slots
@@ -27,9 +27,15 @@ namespace mlxq {
 
 constexpr int kStreamWarps = 16;
 constexpr int kStreamThreads = kStreamWarps * 32;
-constexpr int kDepth = 6;                          // ring stages per warp
 constexpr uint32_t kStageBytes = 512 + 512 + 128;  // codes of half A, of half B, scales
-constexpr uint32_t kRingBytes = kDepth * kStageBytes;
+
+// Stages of a warp's ring: six where latency counts; with more columns four, the
+// room of the others holds activations.
+template <int NT>
+struct Ring {
+    static constexpr int kDepth = NT == 1 ? 6 : 4;
+    static constexpr uint32_t kBytes = kDepth * kStageBytes;
+};
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -558,6 +564,8 @@ constexpr uint32_t kSharedArea = 2176;  // a warp's partial sums awaiting a join
 // All warps of the block call this together.
 template <class F, int NT, class Job>
 __device__ __forceinline__ void shared_phase(const Job& job, uint32_t ring, uint8_t* areas, const XBuffer& xb) {
+    constexpr int kDepth = Ring<NT>::kDepth;
+    constexpr uint32_t kRingBytes = Ring<NT>::kBytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int S = (job.K + F::kStepCols - 1) / F::kStepCols;
     auto chunk_steps = [&](int s) { return min(S, xb.bytes / (64 * F::kPieces * job.cols(s))); };
