@@ -128,10 +128,29 @@ def _ptr(b):
     return b.data_ptr()
 
 
+_current_stream = None
+
+
+def _find_current_stream():
+    """A function that returns torch's current stream as an integer.  Without
+    building a Stream object where torch has the shortcut: 0.5 against 4.4 us a
+    call, of the 10 us that a small call took."""
+    global _current_stream
+    import torch
+    if not torch.cuda.is_available():
+        return lambda: 0
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = torch.cuda.current_device
+    if raw is not None:
+        _current_stream = lambda: raw(device())
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream
+    return _current_stream
+
+
 def _stream(s) -> int:
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else 0
+        return (_current_stream or _find_current_stream())()
     if isinstance(s, int):
         return s
     return s.cuda_stream
