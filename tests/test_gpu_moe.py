@@ -124,6 +124,19 @@ def test_layer_decode_sizes(group):
         check(L.run(dev(xb), 2), want, err)
 
 
+@pytest.mark.parametrize("group", [64, 0], ids=["gs64", "mx4"])
+@pytest.mark.parametrize("m,H", [(3, 32768), (24, 16384)])
+def test_layer_wide_hidden(m, H, group):
+    """More activations than shared memory holds: several chunks of K, refilled for every round of tiles."""
+    L = Layer(m, 2, H, 128, group)
+    xb = synth.activations(L.g, m, H)
+    # columns whose largest values lie in different chunks
+    xb[0, : H // 2] = synth.to_bf16_bits(synth.bf16_bits_to_f32(xb[0, : H // 2]) * np.float32(2.0 ** -12))
+    xb[1, H // 2:] = synth.to_bf16_bits(synth.bf16_bits_to_f32(xb[1, H // 2:]) * np.float32(2.0 ** -12))
+    want, _, err = L.reference(xb, 1)
+    check(L.run(dev(xb), 1), want, err)
+
+
 @pytest.mark.parametrize("m", [5, 40])
 @pytest.mark.parametrize("group", [64, 0], ids=["gs64", "mx4"])
 def test_equal_logits_take_the_lowest_experts(m, group):

@@ -107,7 +107,8 @@ def make(seed, rows, cols, **k):
 
 
 GEMM = [(1, 1, 32), (1, 9, 64), (3, 148, 96), (8, 300, 4128), (9, 17, 160), (16, 4099, 544), (17, 1200, 128),
-        (33, 2500, 1056), (64, 333, 2080), (61, 64, 32), (1, 4096, 4096), (5, 9000, 256), (40, 5003, 96)]
+        (33, 2500, 1056), (64, 333, 2080), (61, 64, 32), (1, 4096, 4096), (5, 9000, 256), (40, 5003, 96),
+        (8, 200, 8192), (2, 150, 36864), (20, 700, 14336), (64, 4099, 4128), (64, 20, 4096), (30, 2000, 64)]
 
 
 @pytest.mark.parametrize("m,N,K", GEMM)
@@ -206,6 +207,71 @@ def test_quantize_then_gemm_on_a_side_stream_and_in_a_graph():
     assert np.array_equal(host_bits(y), eager) and np.array_equal(host_bits(back), eager_back)
 
 
+def test_gemm_rows_of_very_different_sizes():
+    """Each row of X has its own unit: tiny and huge rows side by side, and values of very different size within a row."""
+    N, K = 90, 1312
+    g, codes, scales, h = make(10, N, K)
+    w = ref.values(codes, scales)
+    for m in (3, 18, 50):
+        v = g.standard_normal((m, K)) * 2.0 ** g.integers(-100, 100, (m, 1)) * 2.0 ** g.integers(-30, 1, (m, K))
+        xb = synth.to_bf16_bits(v)
+        x = bits_to_f64(xb)
+        y = torch.empty(m, N, dtype=torch.bfloat16, device="cuda")
+        mq.mlxq_mx4_gemm(h, dev(xb), y, m)
+        want = x @ w.T
+        # and each value is off by at most 2^-25 of its row's largest
+        extra = 2.0 ** -25 * np.abs(x).max(axis=1, keepdims=True) * np.abs(w).sum(axis=1)[None, :]
+        err = np.abs(bits_to_f64(host_bits(y)) - want)
+        assert np.all(err <= bound(np.abs(w), np.abs(x), want, K) + extra), m
+
+
+def test_gemm_graphs_side_by_side():
+    """Batches that take scratch from the pool: two captured graphs replayed on two streams at once."""
+    N, K = 1500, 2080
+    g, codes, scales, h = make(11, N, K)
+    w = ref.values(codes, scales)
+    xs = [synth.activations(g, m, K) for m in (12, 50)]
+    ys = [torch.zeros(x.shape[0], N, dtype=torch.bfloat16, device="cuda") for x in xs]
+    keep = [dev(x) for x in xs]
+    graphs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for x, y, s in zip(keep, ys, streams):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            for _ in range(3):
+                mq.mlxq_mx4_gemm(h, x, y, x.shape[0], s)
+        graphs.append(graph)
+    for _ in range(5):
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for xb, y in zip(xs, ys):
+        x = bits_to_f64(xb)
+        err = np.abs(bits_to_f64(host_bits(y)) - x @ w.T)
+        assert np.all(err <= bound(np.abs(w), np.abs(x), x @ w.T, K))
+
+
+def test_calls_repeat_bit_for_bit():
+    g, codes, scales, h = make(12, 1000, 4128)
+    ac, as_ = ref.random_weight(g, 70, 4128)
+    a = mq.mx4_view(dev(ref.pack(ac)), dev(as_))
+    first = None
+    for _ in range(4):
+        out = []
+        for m in (1, 7, 20, 64):
+            x = dev(synth.activations(synth.rng(m), m, 4128))
+            y = torch.empty(m, 1000, dtype=torch.bfloat16, device="cuda")
+            mq.mlxq_mx4_gemm(h, x, y, m)
+            out.append(host_bits(y))
+        y = torch.empty(70, 1000, dtype=torch.bfloat16, device="cuda")
+        mq.mlxq_mx4_matmul(h, a, y)
+        out.append(host_bits(y))
+        if first is None:
+            first = out
+        assert all(np.array_equal(p, q) for p, q in zip(first, out))
+
+
 def test_gemm_past_32_bits_of_codes():
     """A weight whose codes pass 2^31 bytes: the last rows are read where they are."""
     N, K = 2 ** 20 + 8, 4224
@@ -223,7 +289,8 @@ def test_gemm_past_32_bits_of_codes():
 
 # (m, N, K): both operands in MX4; tiles are 256 x up to 224, k-blocks 256
 MATMUL = [(1, 1, 32), (16, 256, 256), (128, 256, 512), (224, 512, 1024), (5, 300, 96), (130, 260, 288), (300, 1000, 736),
-          (225, 257, 4128), (509, 1100, 544), (64, 4097, 1280), (2000, 3100, 256), (17, 5000, 2048)]
+          (225, 257, 4128), (509, 1100, 544), (64, 4097, 1280), (2000, 3100, 256), (17, 5000, 2048), (1, 300, 8192), (250, 600, 14368),
+          (40, 2000, 4640)]
 
 
 @pytest.mark.parametrize("m,N,K", MATMUL)

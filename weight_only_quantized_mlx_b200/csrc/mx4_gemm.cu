@@ -352,8 +352,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_mx4_gemm_async(const __gr
         cluster.sync();  // all sums are there
         const int rows = hi - lo, n = rows * p.m;
         for (int i = rank * static_cast<int>(blockDim.x) + threadIdx.x; i < n; i += S * static_cast<int>(blockDim.x)) {
-            float s = 0.f;
-            for (int q = 0; q < S; ++q) s += ld_cluster_f32(partial + static_cast<uint32_t>(i) * 4u, static_cast<uint32_t>(q));
+            float v[8];  // all ranks' sums, in flight together
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < S) v[q] = ld_cluster_f32(partial + static_cast<uint32_t>(i) * 4u, static_cast<uint32_t>(q));
+            float s = v[0];
+#pragma unroll
+            for (int q = 1; q < 8; ++q)
+                if (q < S) s += v[q];
             const int c = i / rows, row = i - c * rows;
             p.y[static_cast<int64_t>(c) * p.N + lo + row] = static_cast<uint16_t>(pack_bf16x2(s, 0.f));
         }

@@ -4,7 +4,9 @@
 //
 //   tile: 256 weight rows (two MMA M = 128 halves) x BN activation rows (MMA N,
 //         up to 224), over all of K in k-blocks of 256 columns (one 128-byte row
-//         of codes, four MMAs of K = 64 per half)
+//         of codes, four MMAs of K = 64 per half).  Where tiles leave SMs idle, the
+//         S blocks of a cluster take a range of K of one tile each and add their
+//         sums through distributed shared memory, in rank order.
 //   warp 0      TMA: the codes of both operands (128-byte swizzle)
 //   warp 1      allocates TMEM; one lane copies each k-block's scales into TMEM
 //               (tcgen05.cp) and issues the MMAs
@@ -26,6 +28,8 @@
 //
 // All waits are bounded; after one gives up the producers and the MMA thread
 // issue nothing more and wait (bounded) for what they issued.
+#include <cooperative_groups.h>
+
 #include "device_common.cuh"
 #include "kernels.h"
 #include "mx4_common.cuh"
@@ -54,7 +58,7 @@ struct MatmulParams {
     const uint8_t* w_scales;
     const uint8_t* a_scales;
     int N, m, G;        // weight rows, activation rows, scale bytes per row
-    int BN, num_kb;
+    int BN, num_kb, S;
     uint32_t idesc;
     unsigned int* status;
 };
@@ -156,7 +160,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;  // swizzle atoms
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles_n = (p.N + kBM - 1) / kBM, tiles = tiles_n * ((p.m + p.BN - 1) / p.BN);
-    const int num_kb = p.num_kb;
+    // S == 1: block b takes tiles b, b + gridDim.x, ...; else cluster c takes tile c alone
+    const int S = p.S, rank = static_cast<int>(blockIdx.x) % S, first = static_cast<int>(blockIdx.x) / S;
+    const int stride = S == 1 ? static_cast<int>(gridDim.x) : tiles;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(p.num_kb) * rank / S);
+    const int num_kb = static_cast<int>(static_cast<int64_t>(p.num_kb) * (rank + 1) / S) - kb0;
 
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * static_cast<uint32_t>(s); };                 // codes landed
@@ -200,15 +208,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t bytes = kStageW + static_cast<uint32_t>(p.BN) * 128u;
             bool ok = true;
             int it = 0;
-            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+            for (int tile = first; tile < tiles && ok; tile += stride) {
                 const int n0 = (tile % tiles_n) * kBM, m0 = (tile / tiles_n) * p.BN;
                 for (int kb = 0; kb < num_kb; ++kb, ++it) {
                     const int s = it % kStages;
                     if (it >= kStages) ok = mbar_wait(empty(s), ((it / kStages) - 1) & 1, p.status);
                     if (!ok) break;
                     mbar_arrive_expect_tx(full(s), bytes);
-                    tma_load_2d(W_of(s), &tm_w, kb * 128, n0, full(s), pol);
-                    tma_load_2d(X_of(s), &tm_a, kb * 128, m0, full(s), pol);
+                    tma_load_2d(W_of(s), &tm_w, (kb0 + kb) * 128, n0, full(s), pol);
+                    tma_load_2d(X_of(s), &tm_a, (kb0 + kb) * 128, m0, full(s), pol);
                 }
             }
             // every issued copy has landed before the block may exit
@@ -220,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             bool ok = true;
             int it = 0, t = 0;
-            for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, ++t) {
+            for (int tile = first; tile < tiles && ok; tile += stride, ++t) {
                 if (t >= 1) ok = mbar_wait(acc_empty, (t - 1) & 1, p.status);
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -272,21 +280,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = half * 128 + lane + 32 * i;
-                load_words<WIDE>(v[i], scales, static_cast<int64_t>(r0 + r) * p.G + kb * 8, table, r < span && r0 + r < rows);
+                load_words<WIDE>(v[i], scales, static_cast<int64_t>(r0 + r) * p.G + (kb0 + kb) * 8, table, r < span && r0 + r < rows);
             }
         };
         bool ok = true;
-        int it = 0, ltile = blockIdx.x, lkb = 0;  // what is loaded next
+        int it = 0, ltile = first, lkb = 0;  // what is loaded next
         uint32_t v[2][4][kWords];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (ltile < tiles) load(v[i], ltile, lkb);
             if (++lkb == num_kb) {
                 lkb = 0;
-                ltile += gridDim.x;
+                ltile += stride;
             }
         }
-        for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        for (int tile = first; tile < tiles && ok; tile += stride) {
             const int r0 = first_row(tile);
             for (int kb = 0; kb < num_kb; ++kb, ++it) {
                 const int s = it % kStages;
@@ -294,15 +302,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = half * 128 + lane + 32 * i;
-                    c[i] = scale_bytes<WIDE>(v[0][i], scales, static_cast<int64_t>(r0 + r) * p.G + kb * 8, table, r < span && r0 + r < rows,
-                                             p.G - kb * 8);
+                    c[i] = scale_bytes<WIDE>(v[0][i], scales, static_cast<int64_t>(r0 + r) * p.G + (kb0 + kb) * 8, table,
+                                             r < span && r0 + r < rows, p.G - (kb0 + kb) * 8);
 #pragma unroll
                     for (int j = 0; j < kWords; ++j) v[0][i][j] = v[1][i][j];
                 }
                 if (ltile < tiles) load(v[1], ltile, lkb);
                 if (++lkb == num_kb) {
                     lkb = 0;
-                    ltile += gridDim.x;
+                    ltile += stride;
                 }
                 if (it >= kStages) ok = mbar_wait(empty(s), ((it / kStages) - 1) & 1, p.status);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -323,12 +331,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e = warp - kFirstEpilogue, half = e >> 2, quad = warp & 3;  // TMEM lanes 32 quad ..
         const int64_t N = p.N;
         int t = 0;
-        for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++t) {
+        for (int tile = first; tile < tiles; tile += stride, ++t) {
             const int n = (tile % tiles_n) * kBM + half * 128 + quad * 32 + lane, m0 = (tile / tiles_n) * p.BN;
             const bool ok = mbar_wait(acc_full, t & 1, p.status);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(half) * kAccCols;
+            if (S > 1) {  // the one tile's sums, [BN][256] over the stages, which no copy or MMA uses any more
+                const uint32_t dst = base + static_cast<uint32_t>(half * 128 + quad * 32 + lane) * 4u;
+                for (int c = 0; c < p.BN; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(src + static_cast<uint32_t>(c), r);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + static_cast<uint32_t>(c + i) * 1024u), "r"(r[i]) : "memory");
+                }
+                break;
+            }
             uint32_t y[kMaxBN / 2];  // BF16 pairs: columns 2i, 2i + 1
 #pragma unroll
             for (int c = 0; c < kMaxBN / 16; ++c) {
@@ -356,24 +376,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncwarp();
+    if (S > 1) {
+        cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+        cluster.sync();  // all ranges' sums are there
+        const int n0 = (first % tiles_n) * kBM, m0 = (first / tiles_n) * p.BN, cols = min(p.BN, p.m - m0);
+        const int mine = cols > rank ? (cols - rank - 1) / S + 1 : 0;  // activation rows rank, rank + S, ...
+        for (int i = threadIdx.x; i < mine * (kBM / 4); i += kThreads) {
+            const int c = rank + (i >> 6) * S, r = (i & 63) * 4;
+            float4 v[8];  // all ranks' sums of four weight rows, in flight together
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < S)
+                    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+                                 : "=f"(v[q].x), "=f"(v[q].y), "=f"(v[q].z), "=f"(v[q].w)
+                                 : "r"(base + static_cast<uint32_t>(c * kBM + r) * 4u), "r"(q));
+            float4 sum = v[0];
+#pragma unroll
+            for (int q = 1; q < 8; ++q)
+                if (q < S) {
+                    sum.x += v[q].x;
+                    sum.y += v[q].y;
+                    sum.z += v[q].z;
+                    sum.w += v[q].w;
+                }
+            uint16_t* out = p.Y + static_cast<int64_t>(m0 + c) * p.N + n0 + r;
+            const uint32_t lo = pack_bf16x2(sum.x, sum.y), hi = pack_bf16x2(sum.z, sum.w);
+            if (n0 + r < p.N) out[0] = static_cast<uint16_t>(lo);
+            if (n0 + r + 1 < p.N) out[1] = static_cast<uint16_t>(lo >> 16);
+            if (n0 + r + 2 < p.N) out[2] = static_cast<uint16_t>(hi);
+            if (n0 + r + 3 < p.N) out[3] = static_cast<uint16_t>(hi >> 16);
+        }
+        cluster.sync();  // no block leaves while a peer reads its sums
+    }
     __syncthreads();
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-// Activation rows per tile: the multiple of 16 that ends first, counting a
-// k-block as its bytes (256 + BN rows of codes: they bound the kernel).
-int pick_bn(int64_t m, int64_t N, int sms) {
-    int best = 16;
-    int64_t best_cost = INT64_MAX;
-    for (int bn = 16; bn <= kMaxBN; bn += 16) {
-        const int64_t tiles = ((N + kBM - 1) / kBM) * ((m + bn - 1) / bn);
-        const int64_t cost = ((tiles + sms - 1) / sms) * (kBM + bn);
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = bn;
+// Activation rows per tile and ranges of K: the pair that ends first.  A k-block
+// takes about 0.72 us and 0.9 ns per activation row (measured 0.8 at 64 rows, 0.9
+// at 224: an MMA of few columns is hardly shorter than one of many), so tiles are
+// wide and idle SMs are filled by splitting K, which costs about 3 us and the
+// exchange of sums.
+void pick_plan(int64_t m, int64_t N, int num_kb, int sms, int* bn_out, int* s_out) {
+    int64_t best = INT64_MAX;
+    for (int S = 1; S <= 8 && S <= num_kb; S *= 2) {
+        for (int bn = 16; bn <= kMaxBN; bn += 16) {
+            if (S > 1 && bn * kBM * 4 > static_cast<int>(kStages * kStageBytes)) continue;
+            const int64_t tiles = ((N + kBM - 1) / kBM) * ((m + bn - 1) / bn);
+            // (a cluster wants its SMs in one GPC: not every SM finds one)
+            if (S > 1 && tiles * S > sms - 4 * S) continue;
+            const int64_t kb = (num_kb + S - 1) / S, waves = S > 1 ? 1 : (tiles + sms - 1) / sms;
+            const int64_t cost = waves * kb * (720 + bn * 9 / 10) + (S > 1 ? 3000 + bn * 10 : 0);  // ns
+            if (cost < best) {
+                best = cost;
+                *bn_out = bn;
+                *s_out = S;
+            }
         }
     }
-    return best;
 }
 
 template <bool WIDE>
@@ -382,7 +443,21 @@ cudaError_t launch(unsigned grid, const CUtensorMap& tm_w, const CUtensorMap& tm
     const size_t smem = kStages * kStageBytes + 1024;
     cudaError_t e = ensure_dynamic_smem(k_mx4_matmul<WIDE>, smem, configured);
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_mx4_matmul<WIDE>, dim3(grid), dim3(kThreads), smem, stream, tm_w, tm_a, p);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.S);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.S > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_mx4_matmul<WIDE>, tm_w, tm_a, p);
 }
 
 }  // namespace
@@ -397,8 +472,8 @@ cudaError_t launch_mx4_matmul(const Mx4View& w, const Mx4View& a, void* y, cudaS
     p.N = static_cast<int>(w.rows);
     p.m = static_cast<int>(a.rows);
     p.G = static_cast<int>(w.cols / kMxBlock);
-    p.BN = pick_bn(a.rows, w.rows, sms);
     p.num_kb = static_cast<int>((w.cols + kBK - 1) / kBK);
+    pick_plan(a.rows, w.rows, p.num_kb, sms, &p.BN, &p.S);
     const bool a8 = ((reinterpret_cast<uintptr_t>(w.scales) | reinterpret_cast<uintptr_t>(a.scales)) & 7u) == 0;
     const bool wide = p.G % 8 == 0 && a8;
     // kind::mxf4: A and B E2M1 (1), scales UE8M0 (bit 23), N / 8, M / 128
@@ -412,7 +487,7 @@ cudaError_t launch_mx4_matmul(const Mx4View& w, const Mx4View& a, void* y, cudaS
         return cudaErrorInvalidValue;
     const int64_t tiles = ((w.rows + kBM - 1) / kBM) * ((a.rows + p.BN - 1) / p.BN);
     if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;
-    const unsigned grid = static_cast<unsigned>(tiles < sms ? tiles : sms);
+    const unsigned grid = static_cast<unsigned>(p.S > 1 ? tiles * p.S : (tiles < sms ? tiles : sms));
     return wide ? launch<true>(grid, tm_w, tm_a, p, stream) : launch<false>(grid, tm_w, tm_a, p, stream);
 }
 
