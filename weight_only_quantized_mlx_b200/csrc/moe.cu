@@ -178,15 +178,14 @@ struct ExpertParams {
     unsigned int* status;
 };
 
-// The hit experts with their tokens, as entries of up to kMaxCols columns (an
-// expert with more tokens takes several entries: its weights are then streamed
-// once for each).  A slot is token * top_k + choice.  Up to 8 tokens (NT == 1):
+// The hit experts with their tokens, as entries of up to 8 NT columns (an expert
+// with more tokens takes several entries: its weights are then streamed once for
+// each).  A slot is token * top_k + choice.  Up to 8 tokens (NT == 1):
 // column = token, eight columns per entry, -1 where the token did not choose the
 // expert.  Otherwise an entry's slots one after another, padded with -1 to a
 // multiple of 8.
-constexpr int kMaxCols = 32;
 constexpr int kMaxSlots = kMoeMaxTokens * kMoeMaxTopK;
-constexpr int kMaxEntries = kMaxExperts + kMaxSlots / kMaxCols;
+constexpr int kMaxEntries = kMaxExperts + kMaxSlots / 16;
 constexpr int kMaxListed = kMaxSlots + 7 * kMaxExperts;  // lists padded to multiples of 8
 
 struct ExpertLists {
@@ -225,6 +224,7 @@ __device__ __forceinline__ void clear_lists(ExpertLists& L, int E) {
 
 template <int NT>
 __device__ __forceinline__ void build_lists(ExpertLists& L, const int* ids, int slots, int top_k, int E, int I) {
+    constexpr int kMaxCols = 8 * NT;
     const int tid = threadIdx.x, lane = tid & 31;
     for (int s = tid; s < slots; s += kStreamThreads) atomicAdd(&L.count[ids[s]], 1);
     __syncthreads();
@@ -316,7 +316,7 @@ __device__ __forceinline__ bool grid_barrier(unsigned int* count, unsigned int* 
 //                              | down: areas.
 template <int NT>
 struct Smem {
-    static constexpr int kTokens = NT == 1 ? 8 : (NT == 2 ? 16 : kMoeMaxTokens);  // most tokens of a call
+    static constexpr int kTokens = NT == 1 ? 8 : kMoeMaxTokens;  // most tokens of a call
     static constexpr uint32_t kDownArea = NT == 1 ? 2048 : 16 * (kTokens + 4) * 4;  // a warp's sums of the down phase
     static constexpr uint32_t kLists = kStreamWarps * Ring<NT>::kBytes;
     static constexpr uint32_t kAreas = (kLists + sizeof(ExpertLists) + 127) / 128 * 128;
@@ -664,7 +664,9 @@ cudaError_t launch_moe_any(const MoeCall& c, const View& gate, const View& up, c
     const ExpertParams<FG> p{FG::make(gate), FG::make(up), FD::make(down), static_cast<const uint16_t*>(c.x),
                             static_cast<uint16_t*>(c.y), c.experts, c.hidden, c.inter, c.m, c.top_k, ws, device_status_ptr()};
     if (c.m <= 8) return launch_experts<FG, FD, 1>(p, stream);
-    if (c.m <= 16) return launch_experts<FG, FD, 2>(p, stream);
+    // Two column tiles where experts have up to 8 tokens on average: fewer registers,
+    // and the few experts with more than 16 are streamed again.
+    if (c.m <= 16 || c.m * c.top_k <= 8 * c.experts) return launch_experts<FG, FD, 2>(p, stream);
     return launch_experts<FG, FD, 4>(p, stream);
 }
 
