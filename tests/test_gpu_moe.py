@@ -180,6 +180,32 @@ def test_a_bad_token_stays_alone(m, bad):
     assert not torch.isfinite(y[1].float()).any()
 
 
+@pytest.mark.parametrize("m", [1, 3, 8, 12, 40])
+@pytest.mark.parametrize("group", [64, 0], ids=["gs64", "mx4"])
+def test_a_bad_expert_reaches_only_its_tokens(m, group):
+    """Infinite and NaN weights of an expert: tokens that did not choose it get the same bits as before."""
+    E, H, I, k = 8, 128, 64, 2
+    L = Layer(18, E, H, I, group)
+    xb = synth.activations(L.g, m, H)
+    _, ids, _ = L.reference(xb, k)
+    x = dev(xb)
+    clean = L.run(x, k)
+    bad = int(ids[0, 0])
+    hit = (ids == bad).any(dim=1).tolist()
+    for i, per in ((2, H), (0, I), (1, I)):  # down, gate, up
+        if group:
+            scales = L.keep[i][1]
+            scales[bad * per:(bad + 1) * per] = float("nan") if i == 0 else float("inf")
+        else:
+            L.handles[i].tensors[1][bad * per:(bad + 1) * per] = 255
+        y = L.run(x, k)
+        for t in range(m):
+            if hit[t]:
+                assert not torch.isfinite(y[t].float()).any()
+            else:
+                assert torch.equal(y[t], clean[t])
+
+
 def test_output_is_written_exactly():
     L = Layer(15, 8, 192, 64, 64)
     m = 5

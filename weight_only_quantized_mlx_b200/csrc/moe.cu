@@ -405,8 +405,8 @@ struct GateUpJob {
 // y[token][row] = sum over hit experts a and columns k of Wd_a[row, k] h[slot][k]
 // for the block's rows [lo, hi).  Tiles are 16 rows; every expert's slice of a
 // tile goes into one accumulator, so the sum over experts needs no second pass
-// and no atomics: with up to 8 tokens column = token and the fragment itself
-// accumulates, else each warp adds an expert's columns to its own
+// and no atomics: with up to 8 tokens column = token and each expert's fragment
+// is added, where the token chose the expert, else each warp adds an expert's columns to its own
 // [16][tokens] sums in shared memory.  The warps that share a tile join in warp
 // order, so results do not depend on timing.  h is read once or twice per
 // block, so it is not staged: a lane loads the next step's first column tile
@@ -487,6 +487,7 @@ __device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L
             const int tile = tile0 + batch * groups;
             if (tile >= tiles) break;
             float acc[NT][4];
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};  // NT == 1: over the experts
             const uint16_t* xp[NT];  // this lane's rows of h, at its place in a step
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -569,10 +570,22 @@ __device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L
                 else if (NT == 2 || nt == 2) run(std::integral_constant<int, 2>{});
                 else run(std::integral_constant<int, 4>{});
                 row0 = next0;
-                if (NT > 1) scatter(a, nt);
+                if (NT > 1) {
+                    scatter(a, nt);
+                } else {
+                    // a token that did not choose the expert gets nothing of it: zeros
+                    // times an infinite or NaN weight would not be zero
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (cm.slot(a, 2 * t + i) >= 0) {
+                            sum[i] += acc[0][i];
+                            sum[2 + i] += acc[0][2 + i];
+                        }
+                        acc[0][i] = acc[0][2 + i] = 0.f;
+                    }
+                }
             }
-            if (NT == 1)
-                reinterpret_cast<float4*>(area)[batch * 32 + lane] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
+            if (NT == 1) reinterpret_cast<float4*>(area)[batch * 32 + lane] = make_float4(sum[0], sum[1], sum[2], sum[3]);
         }
         group_sync(group, wk);
         const int me = kw * 32 + lane, threads = wk * 32;
