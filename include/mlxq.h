@@ -269,7 +269,9 @@ MLXQ_API int mlxq_mx4_dequant(const mlxq_mx4* w, void* out, uint64_t stream);
 /*
  * mlxq_mx4_gemm.  Y = X W^T with BF16 activations (weight-only).  X: BF16
  * [m, cols] row-major, 16-byte aligned; Y: BF16 [m, rows].  0 <= m <= 64 (m == 0
- * is a no-op; more rows: MLXQ_ERR_UNSUPPORTED, see mlxq_mx4_matmul).
+ * is a no-op; more rows: MLXQ_ERR_UNSUPPORTED, see mlxq_mx4_matmul).  Products
+ * are exact and sums fp32 for activations down to 2^-31 of the largest of their
+ * row; smaller ones are off by at most 2^-39 of it.
  */
 MLXQ_API int mlxq_mx4_gemm(const mlxq_mx4* w, const void* x, void* y, uint32_t m, uint64_t stream);
 
@@ -295,7 +297,8 @@ MLXQ_API int mlxq_mx4_matmul(const mlxq_mx4* w, const mlxq_mx4* a, void* y, uint
  *   mlxq_moe      8-bit weights; hidden and inter multiples of 64, group_size 32,
  *                 64 or 128 (one for gate and up), codes 16-byte and tables
  *                 4-byte aligned.  Weight flags are ignored.
- *   mlxq_mx4_moe  MX4 weights; hidden and inter multiples of 32.
+ *   mlxq_mx4_moe  MX4 weights; hidden and inter multiples of 32.  Activations as in
+ *                 mlxq_mx4_gemm.
  * workspace: device memory, 16-byte aligned, of at least
  * mlxq_moe_workspace_bytes bytes; its contents on entry do not matter.  One call
  * at a time may use it: calls (and captured graphs) that can overlap on the GPU

@@ -206,6 +206,24 @@ def test_a_bad_expert_reaches_only_its_tokens(m, group):
                 assert torch.equal(y[t], clean[t])
 
 
+@pytest.mark.parametrize("m", [2, 30])
+def test_activations_of_a_wide_range(m):
+    """One activation 2^24 times the others under weights that are zero there (MX4)."""
+    E, H, I, k = 4, 128, 96, 2
+    L = Layer(19, E, H, I, 0)
+    L.router_bits[:, 9] = 0
+    L.router = dev(L.router_bits)
+    for i in (0, 1):
+        L.values[i][:, :, 9] = 0
+        L.handles[i].tensors[0][:, 1] &= ~0xF0  # column 9: the second nibble of word 1
+    x = synth.bf16_bits_to_f32(synth.activations(L.g, m, H)).astype(np.float32)
+    x = np.sign(x) * np.clip(np.abs(x), 2.0 ** -6, None)
+    x[:, 9] = 2.0 ** 24
+    xb = synth.to_bf16_bits(x)
+    want, _, err = L.reference(xb, k)
+    check(L.run(dev(xb), k), want, err)
+
+
 def test_output_is_written_exactly():
     L = Layer(15, 8, 192, 64, 64)
     m = 5

@@ -160,6 +160,46 @@ def test_gemm_nan_and_infinity_stay_in_their_rows(m):
     assert np.array_equal(nan, want)
 
 
+@pytest.mark.parametrize("m,K", [(1, 416), (4, 36864), (12, 416), (40, 2080)])
+@pytest.mark.parametrize("ratio", [17, 24, 30])
+def test_gemm_activations_of_a_wide_range(m, K, ratio):
+    """One column of activations 2^ratio times the others, under codes that are zero: what is left
+    is the others' sum, as exact as without it (BF16 values down to 2^-31 of the largest are kept whole)."""
+    N = 90
+    g, codes, scales, h = make(7, N, K)
+    codes[:, 5] = 0
+    h = mq.mx4_view(dev(ref.pack(codes)), dev(scales))
+    w = ref.values(codes, scales)
+    x32 = np.sign(g.standard_normal((m, K))) * g.uniform(1, 2, (m, K))
+    x32[:, 5] = 1.5 * 2.0 ** ratio
+    xb = synth.to_bf16_bits(x32)
+    x = bits_to_f64(xb)
+    y = torch.empty(m, N, dtype=torch.bfloat16, device="cuda")
+    mq.mlxq_mx4_gemm(h, dev(xb), y, m)
+    want = x @ w.T
+    err = np.abs(bits_to_f64(host_bits(y)) - want)
+    assert np.all(err <= bound(np.abs(w), np.abs(x), want, K))
+
+
+@pytest.mark.parametrize("m", [3, 20])
+@pytest.mark.parametrize("e", [-126, -120, -112, 100, 127])
+def test_gemm_activations_at_the_ends_of_the_range(m, e):
+    """The largest activations near the least and the largest BF16 powers of two."""
+    N, K = 50, 160
+    g, codes, scales, h = make(8, N, K)
+    scales[:] = g.integers(117, 123, scales.shape) if e < 0 else g.integers(100, 110, scales.shape)
+    h = mq.mx4_view(dev(ref.pack(codes)), dev(scales))
+    w = ref.values(codes, scales)
+    xb = synth.to_bf16_bits(g.uniform(-1.9, 1.9, (m, K)) * 2.0 ** e)
+    x = bits_to_f64(xb)
+    y = torch.empty(m, N, dtype=torch.bfloat16, device="cuda")
+    mq.mlxq_mx4_gemm(h, dev(xb), y, m)
+    want = x @ w.T
+    err = np.abs(bits_to_f64(host_bits(y)) - want)
+    # (2^-133: the last place of a BF16 result below 2^-126, half of it for each of two roundings)
+    assert np.all(err <= bound(np.abs(w), np.abs(x), want, K) + 2.0 ** -133)
+
+
 def test_gemm_of_no_columns_is_zero_and_empty_outputs_are_nothing():
     y = torch.full((2, 8), 7.0, dtype=torch.bfloat16, device="cuda")
     mq.mlxq_mx4_gemm(mq.mlxq_mx4(None, None, 8, 0), None, y, 2)

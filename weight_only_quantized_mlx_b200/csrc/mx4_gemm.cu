@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kPrepareThreads) k_mx4_prepare(const uint16_t*
     __syncthreads();
     f = top;
     if (threadIdx.x == 0) fields[c] = f;
-    const float inv = __uint_as_float((254u - x_field(f)) << 23);  // 1 / unit
+    const float inv = x_inverse(f);
     for (int q = threadIdx.x; q < pieces; q += kPrepareThreads) {
         const uint4 v = q < K / 8 ? __ldg(src + q) : make_uint4(0u, 0u, 0u, 0u);
         *reinterpret_cast<uint4*>(xp + (static_cast<int64_t>(q >> 2) * m + c) * 64 + (q & 3) * 16) =

@@ -65,10 +65,13 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A column's unit: 2^(f - 127) with f the largest BF16 exponent field among its
-// activations (1 .. 253; infinities and NaN stay what they are in any unit).
-__device__ __forceinline__ uint32_t x_field(uint32_t field) { return min(max(field, 1u), 253u); }
-__device__ __forceinline__ float x_unit(uint32_t field) { return __uint_as_float(x_field(field) << 23); }
+// A column's unit: 2^(f - 141) with f the largest BF16 exponent field among its
+// activations (15 .. 254; infinities and NaN stay what they are in any unit).
+// The largest lies in [2^14, 2^15) units, the upper end of FP16.
+constexpr uint32_t kXTop = 14;
+__device__ __forceinline__ uint32_t x_field(uint32_t field) { return min(max(field, 1u + kXTop), 254u); }
+__device__ __forceinline__ float x_unit(uint32_t field) { return __uint_as_float((x_field(field) - kXTop) << 23); }
+__device__ __forceinline__ float x_inverse(uint32_t field) { return __uint_as_float((254u + kXTop - x_field(field)) << 23); }  // 1 / unit
 
 // ---- 8-bit group-affine weights: 64 columns per step, 16 codes per lane ------------------
 struct Q8Fmt {
@@ -311,10 +314,10 @@ struct Mx4Fmt {
 // above, which has to place bits and multiply), so the codes go to the tensor
 // pipe unscaled: an MMA pair covers one block of 32 columns, and its fp32 result
 // is multiplied by the rows' block scales as it is added to the sums.
-// Activations are held as FP16 in units of their column's largest power of two:
-// a BF16 value's 8 bits fit down to 2^-17 of the column's largest magnitude, and
-// smaller ones are off by at most 2^-25 of it, half an fp32 step.  Sums of |W|
-// alone have to stay inside fp32.
+// Activations are held as FP16 in units that bring their column's largest power of
+// two to 2^14: a BF16 value's 8 bits then fit down to 2^-31 of the column's largest
+// magnitude, so products are exact; smaller values are off by at most 2^-39 of the
+// largest.  A block's sum is below 32 * 6 * 2^15 < 2^23 units.
 struct Mx4HalfFmt : Mx4Fmt {
     // the 16-byte unit of block b in row g sits at unit b ^ (g / 2), so that the
     // 32 lanes' word loads (row g, word t) touch 32 banks
@@ -546,7 +549,7 @@ __device__ __forceinline__ void stage_columns(const XBuffer& xb, int cols, int s
             const int c = u / lots, q = (u - c * lots) * 32 + lane;
             if (q >= per_col) continue;
             const uint32_t at = place(c, q);
-            const float f = __uint_as_float((254u - x_field(xb.field[c])) << 23);  // 1 / unit
+            const float f = x_inverse(xb.field[c]);
             const uint4 v = lds128(at);
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(scaled_half2(v.x, f)), "r"(scaled_half2(v.y, f)),
                          "r"(scaled_half2(v.z, f)), "r"(scaled_half2(v.w, f))
