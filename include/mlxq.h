@@ -27,8 +27,9 @@
  *     overlaps that the library can see are rejected with MLXQ_ERR_INVALID_ARG.
  *   - Device memory: mlxq_load allocates the weight's three buffers.  When
  *     mlxq_gemm splits K over CTAs it takes fp32 partials from a stream-ordered
- *     pool the library owns (allocated and freed in order on `stream`); the
- *     pool keeps its memory between calls.  No other call allocates device
+ *     pool the library owns (allocated and freed in order on `stream`), and
+ *     mlxq_mx4_gemm from there its copy of X where it makes one; the pool
+ *     keeps its memory between calls.  No other call allocates device
  *     memory; mlxq_gemm_noalloc is mlxq_gemm without any allocation.
  */
 #ifndef MLXQ_H
@@ -300,7 +301,7 @@ MLXQ_API int mlxq_mx4_matmul(const mlxq_mx4* w, const mlxq_mx4* a, void* y, uint
  *   mlxq_mx4_moe  MX4 weights; hidden and inter multiples of 32.  Activations as in
  *                 mlxq_mx4_gemm.
  * workspace: device memory, 16-byte aligned, of at least
- * mlxq_moe_workspace_bytes bytes; its contents on entry do not matter.  One call
+ * mlxq_moe_workspace_bytes bytes (0: the layer does not take such sizes); its contents on entry do not matter.  One call
  * at a time may use it: calls (and captured graphs) that can overlap on the GPU
  * need a workspace each.  The call is two kernel launches, the second a
  * cooperative one, which is refused (MLXQ_ERR_CUDA) where the device cannot

@@ -226,5 +226,33 @@ def test_moe_workspace_size():
     assert mq.mlxq_moe_workspace_bytes(4096, 14336, 16, 64) >= 64 * 16 * 14336 * 2
 
 
+def test_moe_workspace_of_sizes_out_of_range_is_nothing():
+    top = 0xFFFFFFFF
+    for args in ((top, 64, 2, 2), (64, top, 2, 2), (64, 64, top, top), (64, 64, 17, 1), (64, 64, 2, 65)):
+        assert mq.mlxq_moe_workspace_bytes(*args) == 0
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Host tensors while the current device is a GPU: refused before anything is launched."""
+    monkeypatch.setattr(mq, "_current_device", lambda: 0)
+    bad = mq.MLXQ_ERR_INVALID_ARG
+    host = mq.mx4_empty(4, 64, "cpu")
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    calls = [lambda h, t: mq.mlxq_mx4_quantize(t, h, 0), lambda h, t: mq.mlxq_mx4_dequant(h, t, 0),
+             lambda h, t: mq.mlxq_mx4_gemm(h, t, 8 * P, 1, 0), lambda h, t: mq.mlxq_mx4_gemm(h, 4 * P, t, 1, 0),
+             lambda h, t: mq.mlxq_mx4_matmul(h, handle(rows=1, codes=16 * P, scales=17 * P), t, 0),
+             lambda h, t: mq.mlxq_mx4_matmul(handle(rows=1, codes=16 * P, scales=17 * P), h, t, 0)]
+    for call in calls:
+        assert code_of(call, handle(4, 64), x) == bad
+        assert code_of(call, host, 4 * P) == bad
+    host_ws = Fake(A[10], 1 << 20)
+    host_ws.device, host_ws.get_device = "cpu", lambda: -1
+    for call in (moe8, moe4):
+        for k in ({"router": torch.zeros(E, H, dtype=torch.bfloat16)}, {"x": torch.zeros(3, H, dtype=torch.bfloat16)},
+                  {"y": torch.zeros(3, H, dtype=torch.bfloat16)}, {"ws": host_ws}):
+            assert code_of(lambda: call(**k)) == bad
+    assert code_of(lambda: moe4(gate=mq.mx4_empty(E * I, H, "cpu"))) == bad
+
+
 def test_struct_layout():
     assert ctypes.sizeof(mq.mlxq_mx4) == 24

@@ -128,43 +128,76 @@ def _ptr(b):
     return b.data_ptr()
 
 
-_current_stream = None
+_raw_stream = None
 
 
-def _find_current_stream():
-    """A function that returns torch's current stream as an integer.  Without
-    building a Stream object where torch has the shortcut: 0.5 against 4.4 us a
-    call, of the 10 us that a small call took."""
-    global _current_stream
+def _find_raw_stream():
+    """A function from a device to torch's current stream there, as an integer.
+    Without building a Stream object where torch has the shortcut: 0.5 against
+    4.4 us a call, of the 10 us that a small call took."""
+    global _raw_stream
     import torch
     if not torch.cuda.is_available():
-        return lambda: 0
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    device = torch.cuda.current_device
-    if raw is not None:
-        _current_stream = lambda: raw(device())
-    else:
-        _current_stream = lambda: torch.cuda.current_stream().cuda_stream
-    return _current_stream
+        return lambda device: 0
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if _raw_stream is None:
+        _raw_stream = lambda device: torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream
 
 
-def _stream(s) -> int:
+def _stream(s, device=None) -> int:
     if s is None:
-        return (_current_stream or _find_current_stream())()
+        return (_raw_stream or _find_raw_stream())(_device() if device is None else device)
     if isinstance(s, int):
         return s
     return s.cuda_stream
 
 
-def _dense(b, dtype: str, name: str, elems: int):
-    """The address of a buffer that holds `elems` contiguous elements of a torch
-    dtype; raw addresses are taken as they are."""
+_current_device = None
+
+
+def _device() -> int:
+    """torch's current device, -1 where there is none."""
+    global _current_device
+    if _current_device is None:
+        import torch
+        if not torch.cuda.is_available():
+            return -1
+        torch.cuda.init()
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _current_device()
+
+
+def _local(b, name: str, device: int) -> None:
+    """Refuse a tensor that is not on the current device: a kernel must not get its address."""
+    if b.get_device() != device:
+        raise MlxqError(MLXQ_ERR_INVALID_ARG, f"{name} is on {b.device}, the current device is cuda:{device}")
+
+
+_bf16 = None  # torch.bfloat16, once it has been seen
+
+
+def _dense(b, name: str, elems: int, device: int):
+    """The address of a buffer that holds `elems` contiguous BF16 elements on the
+    current device; raw addresses are taken as they are."""
+    global _bf16
     if b is None or isinstance(b, int):
         return b
-    if str(b.dtype) != "torch." + dtype or not b.is_contiguous() or b.numel() < elems:
-        raise MlxqError(MLXQ_ERR_INVALID_ARG, f"{name} must be a contiguous {dtype} tensor of at least {elems} elements, "
+    if _bf16 is None and str(b.dtype) == "torch.bfloat16":
+        _bf16 = b.dtype
+    if b.dtype is not _bf16 or not b.is_contiguous() or b.numel() < elems:
+        raise MlxqError(MLXQ_ERR_INVALID_ARG, f"{name} must be a contiguous bfloat16 tensor of at least {elems} elements, "
                                               f"got {b.dtype} {tuple(b.shape)} with strides {tuple(b.stride())}")
+    if b.get_device() != device:
+        _local(b, name, device)
     return b.data_ptr()
+
+
+def _mx4(h: mlxq_mx4, name: str, device: int):
+    """A handle as an argument of a call; its tensors, where it has any, are on the current device."""
+    if h.tensors is not None and h.tensors[0].get_device() != device:
+        _local(h.tensors[0], name, device)
+    return ctypes.byref(h)
 
 
 def _check(rc: int) -> None:
@@ -255,6 +288,8 @@ def mx4_view(codes, scales) -> mlxq_mx4:
                                         f"{tuple(codes.shape)} and {tuple(scales.shape)}")
     if not codes.is_contiguous() or not scales.is_contiguous():
         raise MlxqError(MLXQ_ERR_INVALID_ARG, "MX4 codes and scales must be contiguous")
+    if codes.device != scales.device:
+        raise MlxqError(MLXQ_ERR_INVALID_ARG, f"MX4 codes are on {codes.device} and scales on {scales.device}")
     h = mlxq_mx4(_ptr(codes), _ptr(scales), codes.shape[0], codes.shape[1] * 8)
     h.tensors = (codes, scales)
     return h
@@ -270,48 +305,57 @@ def mx4_empty(rows: int, cols: int, device="cuda") -> mlxq_mx4:
 
 
 def mlxq_mx4_quantize(x_bf16, dst: mlxq_mx4, stream=None) -> None:
-    x = _dense(x_bf16, "bfloat16", "x", dst.rows * dst.cols)
-    _check(lib().mlxq_mx4_quantize(x, ctypes.byref(dst), _stream(stream)))
+    d = _device()
+    x = _dense(x_bf16, "x", dst.rows * dst.cols, d)
+    _check(lib().mlxq_mx4_quantize(x, _mx4(dst, "dst", d), _stream(stream, d)))
 
 
 def mlxq_mx4_dequant(w: mlxq_mx4, out, stream=None) -> None:
-    out = _dense(out, "bfloat16", "out", w.rows * w.cols)
-    _check(lib().mlxq_mx4_dequant(ctypes.byref(w), out, _stream(stream)))
+    d = _device()
+    out = _dense(out, "out", w.rows * w.cols, d)
+    _check(lib().mlxq_mx4_dequant(_mx4(w, "w", d), out, _stream(stream, d)))
 
 
 def mlxq_mx4_gemm(w: mlxq_mx4, x, y, m: int, stream=None) -> None:
-    x, y = _dense(x, "bfloat16", "X", m * w.cols), _dense(y, "bfloat16", "Y", m * w.rows)
-    _check(lib().mlxq_mx4_gemm(ctypes.byref(w), x, y, m, _stream(stream)))
+    d = _device()
+    x, y = _dense(x, "X", m * w.cols, d), _dense(y, "Y", m * w.rows, d)
+    _check(lib().mlxq_mx4_gemm(_mx4(w, "w", d), x, y, m, _stream(stream, d)))
 
 
 def mlxq_mx4_matmul(w: mlxq_mx4, a: mlxq_mx4, y, stream=None) -> None:
-    y = _dense(y, "bfloat16", "Y", a.rows * w.rows)
-    _check(lib().mlxq_mx4_matmul(ctypes.byref(w), ctypes.byref(a), y, _stream(stream)))
+    d = _device()
+    y = _dense(y, "Y", a.rows * w.rows, d)
+    _check(lib().mlxq_mx4_matmul(_mx4(w, "w", d), _mx4(a, "a", d), y, _stream(stream, d)))
 
 
 def mlxq_moe_workspace_bytes(hidden: int, inter: int, top_k: int, m: int) -> int:
     return lib().mlxq_moe_workspace_bytes(hidden, inter, top_k, m)
 
 
-def _moe(fn, hidden, router, gate, up, down, experts, top_k, x, y, m, workspace, stream, flags):
-    router = _dense(router, "bfloat16", "router", experts * hidden)
-    x, y = _dense(x, "bfloat16", "x", m * hidden), _dense(y, "bfloat16", "y", m * hidden)
+def _moe(fn, hidden, router, weights, experts, top_k, x, y, m, workspace, stream, flags, d):
+    router = _dense(router, "router", experts * hidden, d)
+    x, y = _dense(x, "x", m * hidden, d), _dense(y, "y", m * hidden, d)
     if not hasattr(workspace, "data_ptr") or not workspace.is_contiguous():
         raise MlxqError(MLXQ_ERR_INVALID_ARG, "workspace must be a contiguous tensor")
-    _check(fn(router, ctypes.byref(gate), ctypes.byref(up), ctypes.byref(down), experts, top_k, flags, x, y, m,
-              workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+    if hasattr(workspace, "get_device"):
+        _local(workspace, "workspace", d)
+    _check(fn(router, *weights, experts, top_k, flags, x, y, m, workspace.data_ptr(),
+              workspace.numel() * workspace.element_size(), _stream(stream, d)))
 
 
 def mlxq_moe(router, gate: mlxq_weight, up: mlxq_weight, down: mlxq_weight, experts: int, top_k: int, x, y, m: int,
              workspace, stream=None, flags: int = 0) -> None:
     """workspace: a device tensor of at least mlxq_moe_workspace_bytes(...) bytes, for one call at a time."""
-    _moe(lib().mlxq_moe, gate.in_features, router, gate, up, down, experts, top_k, x, y, m, workspace, stream, flags)
+    weights = [ctypes.byref(h) for h in (gate, up, down)]
+    _moe(lib().mlxq_moe, gate.in_features, router, weights, experts, top_k, x, y, m, workspace, stream, flags, _device())
 
 
 def mlxq_mx4_moe(router, gate: mlxq_mx4, up: mlxq_mx4, down: mlxq_mx4, experts: int, top_k: int, x, y, m: int,
                  workspace, stream=None, flags: int = 0) -> None:
     """workspace: a device tensor of at least mlxq_moe_workspace_bytes(...) bytes, for one call at a time."""
-    _moe(lib().mlxq_mx4_moe, gate.cols, router, gate, up, down, experts, top_k, x, y, m, workspace, stream, flags)
+    d = _device()
+    weights = [_mx4(gate, "gate", d), _mx4(up, "up", d), _mx4(down, "down", d)]
+    _moe(lib().mlxq_mx4_moe, gate.cols, router, weights, experts, top_k, x, y, m, workspace, stream, flags, d)
 
 
 class MlxInt8Weight:

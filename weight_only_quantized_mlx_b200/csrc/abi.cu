@@ -829,7 +829,9 @@ int mlxq_mx4_matmul(const mlxq_mx4* w, const mlxq_mx4* a, void* y, uint64_t stre
 
 // ---- mixture-of-experts layer -----------------------------------------------------------------
 size_t mlxq_moe_workspace_bytes(uint32_t hidden, uint32_t inter, uint32_t top_k, uint32_t m) {
-    (void)hidden;
+    // (what the layer does not take needs no workspace, and must not overflow here)
+    if (hidden > kMoeMaxDim || inter > kMoeMaxDim || top_k > static_cast<uint32_t>(kMoeMaxTopK) || m > static_cast<uint32_t>(kMoeMaxTokens))
+        return 0;
     return moe_workspace_bytes(inter, static_cast<int64_t>(m) * top_k);
 }
 
