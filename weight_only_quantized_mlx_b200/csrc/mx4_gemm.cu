@@ -102,14 +102,21 @@ constexpr uint32_t kPartialBytes = 32 * 1024;  // S > 1: fp32 sums of a cluster'
 constexpr int kMaxXStages = 16;
 constexpr uint32_t kAsyncTotal = 227 * 1024 - 512;
 
-// Shared memory: weight rings | areas | units | sums (S > 1) | steps of X.  Four
-// stages a warp's ring (six measured no faster, and take the room of steps of X).
+// Shared memory: weight rings | areas | units | sums (S > 1) | steps of X.
 template <int NT>
 struct AsyncSmem {
+    // A warp's tile is MT times 16 rows.  From four column tiles on, two: a piece of
+    // X is read from shared memory once for both, and eight warps have the registers
+    // for their sums (28672 x 8192, 32 rows: 99 -> 91 us, 64 rows: 189 -> 175; at 16
+    // rows 67 -> 66, but 4096 x 4096 13 -> 14).
+    static constexpr int MT = NT <= 2 ? 1 : 2;
+    static constexpr int kLogWarps = NT <= 2 ? 4 : 3;
+    static constexpr int kWarps = 1 << kLogWarps, kThreads = 32 * kWarps;
     static constexpr int kDepth = 4;
-    static constexpr uint32_t kRing = kDepth * kStageBytes;
-    static constexpr uint32_t kAreas = kStreamWarps * kRing;
-    static constexpr uint32_t kFields = kAreas + kStreamWarps * kSharedArea;
+    static constexpr uint32_t kStage = MT * kStageBytes;
+    static constexpr uint32_t kRing = kDepth * kStage;
+    static constexpr uint32_t kAreas = kWarps * kRing;
+    static constexpr uint32_t kFields = kAreas + kWarps * kSharedArea;
     static constexpr uint32_t kX = kFields + kMx4GemmMaxM * 4;
     static_assert(kAsyncTotal - kX - kPartialBytes >= 2u * NT * 8 * 256, "two steps of X");
 };
@@ -149,7 +156,7 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kStreamThreads, 1) k_mx4_gemm_async(const __grid_constant__ AsyncParams p) {
+__global__ void __launch_bounds__(AsyncSmem<NT>::kThreads, 1) k_mx4_gemm_async(const __grid_constant__ AsyncParams p) {
     using F = Mx4HalfFmt;
     using M = AsyncSmem<NT>;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -163,7 +170,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_mx4_gemm_async(const __gr
     const int all_steps = (p.K + F::kStepCols - 1) / F::kStepCols;
     const int st0 = static_cast<int>(static_cast<int64_t>(all_steps) * rank / S);
     const int steps = static_cast<int>(static_cast<int64_t>(all_steps) * (rank + 1) / S) - st0;
-    const int tiles = (hi - lo + 15) / 16;
+    constexpr int MT = M::MT, kRows = 16 * MT;
+    const int tiles = (hi - lo + kRows - 1) / kRows;
     const uint32_t step_bytes = static_cast<uint32_t>(p.m) * 256u;
     const uint32_t partial = smem_u32(smem) + M::kX, x0 = partial + (S > 1 ? kPartialBytes : 0u);
     const int room = min(static_cast<int>((smem_u32(smem) + kAsyncTotal - x0) / step_bytes), kMaxXStages);
@@ -175,12 +183,12 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_mx4_gemm_async(const __gr
     // barrier's parity a phase early), and at least twice it.
     int lw;
     {
-        const int i = min(lane, 4);
-        int cost = ((tiles + (kStreamWarps >> i) - 1) >> (4 - i)) * (((steps + (1 << i) - 1) >> i) + (i > 0 ? 2 : 0));
+        const int i = min(lane, M::kLogWarps);
+        int cost = ((tiles + (M::kWarps >> i) - 1) >> (M::kLogWarps - i)) * (((steps + (1 << i) - 1) >> i) + (i > 0 ? 2 : 0));
         if ((2 << i) > room && i > 0) cost = 0x0FFFFFFF;
         lw = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(min(cost, 0x0FFFFFFF)) << 3 | static_cast<uint32_t>(i)) & 7u);
     }
-    const int wk = 1 << lw, groups = kStreamWarps >> lw, stages = room >> lw << lw;
+    const int wk = 1 << lw, groups = M::kWarps >> lw, stages = room >> lw << lw;
     const int rounds = (tiles + groups - 1) / groups;
     auto full = [&](int s) { return smem_u32(&bars[s]); };
     auto empty = [&](int s) { return smem_u32(&bars[kMaxXStages + s]); };
@@ -217,30 +225,34 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_mx4_gemm_async(const __gr
         const int own = kw < steps ? (steps - kw + wk - 1) >> lw : 0;
         int ptile = own > 0 ? group : tiles, pleft = 0;
         uint32_t pslot = ring, cslot = ring;
-        F::Feed feed;
+        F::Feed feed[MT];
         auto seek = [&]() {
             pleft = 0;
             if (ptile < tiles) {
-                const int r = lo + ptile * 16 + g;
-                F::start(feed, p.w, p.w, r, r + 8, r < hi, r + 8 < hi, lane, st0 + kw);
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                    const int r = lo + ptile * kRows + 16 * j + g;
+                    F::start(feed[j], p.w, p.w, r, r + 8, r < hi, r + 8 < hi, lane, st0 + kw);
+                }
                 pleft = own;
             }
         };
         seek();
         auto issue = [&]() {
             if (pleft > 0) {
-                F::issue(p.w, feed, pslot, lane, wk);
+#pragma unroll
+                for (int j = 0; j < MT; ++j) F::issue(p.w, feed[j], pslot + j * kStageBytes, lane, wk);
                 if (--pleft == 0) {
                     ptile += groups;
                     seek();
                 }
             }
             cp_async_commit();
-            pslot = pslot == ring + M::kRing - kStageBytes ? ring : pslot + kStageBytes;
+            pslot = pslot == ring + M::kRing - M::kStage ? ring : pslot + M::kStage;
         };
 #pragma unroll 1
         for (int i = 0; i < M::kDepth - 1; ++i) issue();
-        for (int c = threadIdx.x; c < p.m; c += kStreamThreads) field[c] = p.field[c];
+        for (int c = threadIdx.x; c < p.m; c += M::kThreads) field[c] = p.field[c];
         __syncthreads();  // the fields are there
 
         const int nt = (p.m + 7) / 8;
@@ -248,8 +260,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_mx4_gemm_async(const __gr
         uint32_t xo[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) xo[n] = static_cast<uint32_t>(min(n * 8 + g, p.m - 1)) * 64u + static_cast<uint32_t>(t) * 16u;
-        auto store = [&](int tile, int n, int l, const float4& v) {
-            const int r = tile * 16 + (l >> 2), c = n * 8 + 2 * (l & 3), rows = hi - lo;
+        auto store = [&](int r0, int n, int l, const float4& v) {
+            const int r = r0 + (l >> 2), c = n * 8 + 2 * (l & 3), rows = hi - lo;
             const float s[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -268,77 +280,78 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_mx4_gemm_async(const __gr
         for (int r = 0; r < rounds; ++r) {
             const int tile = r * groups + group;
             const bool live = tile < tiles;
-            float acc[NT][4];
+            float acc[MT][NT][4];
+            uint32_t key[MT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-            const uint32_t key = F::row_key(p.w, static_cast<uint32_t>(lo + tile * 16 + g));
+            for (int j = 0; j < MT; ++j) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) acc[j][n][0] = acc[j][n][1] = acc[j][n][2] = acc[j][n][3] = 0.f;
+                key[j] = F::row_key(p.w, static_cast<uint32_t>(lo + tile * kRows + 16 * j + g));
+            }
             bool plain = true;  // sums are in the columns' units
-            auto run = [&](auto count) {
-                constexpr int N = decltype(count)::value < NT ? decltype(count)::value : NT;
 #pragma unroll 1
-                for (int k = kw; k < padded; k += wk) {
-                    const int it = r * padded + k;
-                    // The stage of this warp's last step gets its next contents as soon as
-                    // all groups have read it: one warp of each kw sees to it, the groups
-                    // taking turns.
-                    const int next = it + stages - wk;
-                    if (it >= wk && next < total && ((next >> lw) & (groups - 1)) == group && ok) {
-                        const int s = stage >= wk ? stage - wk : stage - wk + stages;
-                        ok = mbar_wait(empty(s), stage >= wk ? parity : parity ^ 1u, p.status);
-                        if (lane == 0 && ok) feed_x(s, k + ahead < padded ? k + ahead : k + ahead - padded);
-                        __syncwarp();
-                    }
-                    // after a wait has given up there are no more, the control flow goes on
-                    if (ok) ok = mbar_wait(full(stage), parity, p.status);
-                    if (live && k < steps) {
-                        cp_async_wait<M::kDepth - 2>();
-                        __syncwarp();  // the copies of all lanes have landed; the slot refilled below is read out
-                        issue();
-                        F::consume_shared<NT, N>(p.w, cslot, lane, key, st0 + k, acc, x0 + static_cast<uint32_t>(stage) * step_bytes,
-                                                 piece_stride, xo, plain, field, p.m);
-                        cslot = cslot == ring + M::kRing - kStageBytes ? ring : cslot + kStageBytes;
-                    }
+            for (int k = kw; k < padded; k += wk) {
+                const int it = r * padded + k;
+                // The stage of this warp's last step gets its next contents as soon as
+                // all groups have read it: one warp of each kw sees to it, the groups
+                // taking turns.
+                const int next = it + stages - wk;
+                if (it >= wk && next < total && ((next >> lw) & (groups - 1)) == group && ok) {
+                    const int s = stage >= wk ? stage - wk : stage - wk + stages;
+                    ok = mbar_wait(empty(s), stage >= wk ? parity : parity ^ 1u, p.status);
+                    if (lane == 0 && ok) feed_x(s, k + ahead < padded ? k + ahead : k + ahead - padded);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(empty(stage));
-                    stage += wk;
-                    if (stage >= stages) {
-                        stage -= stages;
-                        parity ^= 1u;
-                    }
                 }
-            };
-            if (NT == 1 || nt == 1) run(std::integral_constant<int, 1>{});
-            else if (NT == 2 || nt == 2) run(std::integral_constant<int, 2>{});
-            else if (NT == 4 || nt <= 4) run(std::integral_constant<int, 4>{});
-            else run(std::integral_constant<int, 8>{});
+                // after a wait has given up there are no more, the control flow goes on
+                if (ok) ok = mbar_wait(full(stage), parity, p.status);
+                if (live && k < steps) {
+                    cp_async_wait<M::kDepth - 2>();
+                    __syncwarp();  // the copies of all lanes have landed; the slot refilled below is read out
+                    issue();
+                    F::consume_tiles<MT, NT, NT>(p.w, cslot, lane, key, st0 + k, acc, x0 + static_cast<uint32_t>(stage) * step_bytes,
+                                                piece_stride, xo, plain, field, p.m);
+                    cslot = cslot == ring + M::kRing - M::kStage ? ring : cslot + M::kStage;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty(stage));
+                stage += wk;
+                if (stage >= stages) {
+                    stage -= stages;
+                    parity ^= 1u;
+                }
+            }
             if (!live) continue;
-            if (plain) F::to_numbers<NT>(acc, field, p.m, t);
 #pragma unroll
-            for (int n0 = 0; n0 < NT; n0 += kJoin) {
-                if (n0 >= nt) break;
-                if (wk == 1) {
+            for (int j = 0; j < MT; ++j) {
+                const int r0 = tile * kRows + 16 * j;
+                if (plain) F::to_numbers<NT>(acc[j], field, p.m, t);
+#pragma unroll
+                for (int n0 = 0; n0 < NT; n0 += kJoin) {
+                    if (n0 >= nt) break;
+                    if (wk == 1) {
+#pragma unroll
+                        for (int n = n0; n < n0 + kJoin; ++n)
+                            if (n < nt) store(r0, n, lane, make_float4(acc[j][n][0], acc[j][n][1], acc[j][n][2], acc[j][n][3]));
+                        continue;
+                    }
 #pragma unroll
                     for (int n = 0; n < kJoin; ++n)
-                        if (n0 + n < nt) store(tile, n0 + n, lane, make_float4(acc[n0 + n][0], acc[n0 + n][1], acc[n0 + n][2], acc[n0 + n][3]));
-                    continue;
-                }
-#pragma unroll
-                for (int n = 0; n < kJoin; ++n)
-                    area[n * 32 + lane] = make_float4(acc[n0 + n][0], acc[n0 + n][1], acc[n0 + n][2], acc[n0 + n][3]);
-                group_sync(group, wk);
-                for (int i = kw * 32 + lane; i < kJoin * 32; i += wk * 32) {
-                    if (n0 + (i >> 5) >= nt) continue;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int w = 0; w < wk; ++w) {
-                        const float4 q = group_area[w * kAreaVecs + i];
-                        v.x += q.x;
-                        v.y += q.y;
-                        v.z += q.z;
-                        v.w += q.w;
+                        area[n * 32 + lane] = make_float4(acc[j][n0 + n][0], acc[j][n0 + n][1], acc[j][n0 + n][2], acc[j][n0 + n][3]);
+                    group_sync(group, wk);
+                    for (int i = kw * 32 + lane; i < kJoin * 32; i += wk * 32) {
+                        if (n0 + (i >> 5) >= nt) continue;
+                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int w = 0; w < wk; ++w) {
+                            const float4 q = group_area[w * kAreaVecs + i];
+                            v.x += q.x;
+                            v.y += q.y;
+                            v.z += q.z;
+                            v.w += q.w;
+                        }
+                        store(r0, n0 + (i >> 5), i & 31, v);
                     }
-                    store(tile, n0 + (i >> 5), i & 31, v);
+                    group_sync(group, wk);
                 }
-                group_sync(group, wk);
             }
         }
         cp_async_wait<0>();
@@ -390,7 +403,7 @@ cudaError_t launch_async(AsyncParams p, cudaStream_t stream) {
     cudaError_t e = ensure_dynamic_smem(k_mx4_gemm_async<NT>, kAsyncTotal, configured);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.blockDim = dim3(kStreamThreads);
+    cfg.blockDim = dim3(AsyncSmem<NT>::kThreads);
     cfg.dynamicSmemBytes = kAsyncTotal;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -401,11 +414,14 @@ cudaError_t launch_async(AsyncParams p, cudaStream_t stream) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
 
-    // S: the one that ends first by a model in cycles of an SM - the copies of X at
-    // some 25 bytes a cycle, the products of a step, the weight at its share of
-    // HBM, and the exchange of sums.
+    // S: the one that ends first by a model in cycles of an SM - the products of a
+    // tile's steps (measured at 28672 x 8192) or the weight at its share of HBM, the
+    // copies of X at some 25 bytes a cycle, about half of them hidden, and the
+    // exchange of sums.  It picks what measured best at 1024 x 4096 (64 rows: S = 8
+    // 18.5 us, 1 23.6), 4096 x 14336 (S = 4 51 us, 2 63, 1 60) and 4096 x 4096 (S = 1
+    // 24.2 us, 4 24.8).
     const int steps = (p.K + Mx4HalfFmt::kStepCols - 1) / Mx4HalfFmt::kStepCols;
-    const int per_step = NT == 1 ? 50 : (NT == 2 ? 75 : (NT == 4 ? 110 : 200));
+    const int per_step = NT == 1 ? 80 : (NT == 2 ? 130 : (NT == 4 ? 340 : 700));
     int64_t best = INT64_MAX;
     unsigned grid = 1;
     for (int S = 1; S <= 8 && S <= steps; S *= 2) {
@@ -416,11 +432,12 @@ cudaError_t launch_async(AsyncParams p, cudaStream_t stream) {
         if (clusters > (p.N + 7) / 8) clusters = (p.N + 7) / 8;
         const int64_t rows = (p.N + clusters - 1) / clusters;
         if (S > 1 && (rows + 1) * p.m * 4 > kPartialBytes) continue;
-        const int64_t own = (steps + S - 1) / S, tiles = (rows + 15) / 16;
-        int64_t cost = static_cast<int64_t>(p.m) * own * 256 / 25;
-        if (tiles * own * per_step > cost) cost = tiles * own * per_step;
+        constexpr int kRows = 16 * AsyncSmem<NT>::MT;
+        const int64_t own = (steps + S - 1) / S, tiles = (rows + kRows - 1) / kRows;
+        int64_t cost = tiles * own * per_step;
         if (rows * own * 3 > cost) cost = rows * own * 3;
-        if (S > 1) cost += 3000;
+        cost += p.m * own * 6;
+        if (S > 1) cost += 3000 + rows * p.m;
         if (cost < best) {
             best = cost;
             p.S = S;

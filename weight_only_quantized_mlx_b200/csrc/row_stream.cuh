@@ -334,72 +334,103 @@ struct Mx4HalfFmt : Mx4Fmt {
     // numbers, for the rest of the tile, at the first step with a scale outside
     // 2^-63 .. 2^64: there each product meets scale and unit in the order that
     // does not leave fp32 on the way.
-    template <int NT, int N>
-    static __device__ __forceinline__ void consume_shared(const Mat& w, uint32_t slot, int lane, uint32_t key, int step,
-                                                          float (&acc)[NT][4], uint32_t x, uint32_t piece_stride,
-                                                          const uint32_t (&xo)[NT], bool& plain, const uint32_t* field, int cols) {
+    // MT tiles of 16 rows, their stages one behind the other: each piece of the
+    // activations is read once for all of them.
+    template <int MT, int NT, int N>
+    static __device__ __forceinline__ void consume_tiles(const Mat& w, uint32_t slot, int lane, const uint32_t (&key)[MT], int step,
+                                                         float (&acc)[MT][NT][4], uint32_t x, uint32_t piece_stride,
+                                                         const uint32_t (&xo)[NT], bool& plain, const uint32_t* field, int cols) {
         const int g = lane >> 2, t = lane & 3;
-        const uint4 tb = lds128(slot + 1024u + static_cast<uint32_t>(lane & ~3) * 4u);
-        uint32_t ea = __funnelshift_r(tb.x, tb.y, key), eb = __funnelshift_r(tb.z, tb.w, key);
         const int left = w.G - 4 * step;  // blocks left in the row; behind it codes are zeros, and scales must not be NaN
+        uint32_t ea[MT], eb[MT], mid = 0x80808080u;  // the two top bits of every byte differ: 64 .. 191
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const uint4 tb = lds128(slot + j * kStageBytes + 1024u + static_cast<uint32_t>(lane & ~3) * 4u);
+            ea[j] = __funnelshift_r(tb.x, tb.y, key[j]);
+            eb[j] = __funnelshift_r(tb.z, tb.w, key[j]);
+        }
         if (left < 4) {
             const uint32_t keep = (1u << (8 * left)) - 1u;
-            ea = (ea & keep) | (0x7F7F7F7Fu & ~keep);
-            eb = (eb & keep) | (0x7F7F7F7Fu & ~keep);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                ea[j] = (ea[j] & keep) | (0x7F7F7F7Fu & ~keep);
+                eb[j] = (eb[j] & keep) | (0x7F7F7F7Fu & ~keep);
+            }
         }
-        // the two top bits of every byte differ: 64 .. 191
-        const uint32_t mid = (ea ^ (ea << 1)) & (eb ^ (eb << 1)) & 0x80808080u;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) mid &= (ea[j] ^ (ea[j] << 1)) & (eb[j] ^ (eb[j] << 1));
         if (plain && !__all_sync(0xFFFFFFFFu, mid == 0x80808080u)) {
             plain = false;
-            to_numbers<NT>(acc, field, cols, t);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) to_numbers<NT>(acc[j], field, cols, t);
         }
-        float sa[4], sb[4];
-        e8m0x4(ea, sa);
-        e8m0x4(eb, sb);
+        float sa[MT][4], sb[MT][4];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            e8m0x4(ea[j], sa[j]);
+            e8m0x4(eb[j], sb[j]);
+        }
         // block b of row g, word t: bits 4 and 5 of the address hold b ^ (g / 2)
         const uint32_t row = slot + static_cast<uint32_t>(g * 64 + ((g >> 1) & 3) * 16 + t * 4);
         if (plain) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 const uint32_t at = row ^ static_cast<uint32_t>(b * 16);
-                uint32_t a[4], c[4];
-                e2m1x8_f16(lds32(at), a);
-                e2m1x8_f16(lds32(at + 512u), c);
+                uint32_t a[MT][4], c[MT][4];
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                    e2m1x8_f16(lds32(at + j * kStageBytes), a[j]);
+                    e2m1x8_f16(lds32(at + j * kStageBytes + 512u), c[j]);
+                }
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
                     const uint4 v = lds128(x + static_cast<uint32_t>(b) * piece_stride + xo[n]);
-                    float d[4];
-                    mma_f16_first(d, a[0], c[0], a[1], c[1], v.x, v.y);
-                    mma_f16(d, a[2], c[2], a[3], c[3], v.z, v.w);
-                    acc[n][0] = __fmaf_rn(d[0], sa[b], acc[n][0]);
-                    acc[n][1] = __fmaf_rn(d[1], sa[b], acc[n][1]);
-                    acc[n][2] = __fmaf_rn(d[2], sb[b], acc[n][2]);
-                    acc[n][3] = __fmaf_rn(d[3], sb[b], acc[n][3]);
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) {
+                        float d[4];
+                        mma_f16_first(d, a[j][0], c[j][0], a[j][1], c[j][1], v.x, v.y);
+                        mma_f16(d, a[j][2], c[j][2], a[j][3], c[j][3], v.z, v.w);
+                        acc[j][n][0] = __fmaf_rn(d[0], sa[j][b], acc[j][n][0]);
+                        acc[j][n][1] = __fmaf_rn(d[1], sa[j][b], acc[j][n][1]);
+                        acc[j][n][2] = __fmaf_rn(d[2], sb[j][b], acc[j][n][2]);
+                        acc[j][n][3] = __fmaf_rn(d[3], sb[j][b], acc[j][n][3]);
+                    }
                 }
             }
         } else {
 #pragma unroll 1
             for (int b = 0; b < 4; ++b) {
-                const uint32_t at = row ^ static_cast<uint32_t>(b * 16);
-                uint32_t a[4], c[4];
-                e2m1x8_f16(lds32(at), a);
-                e2m1x8_f16(lds32(at + 512u), c);
-                const float s0 = b == 0 ? sa[0] : (b == 1 ? sa[1] : (b == 2 ? sa[2] : sa[3]));
-                const float s1 = b == 0 ? sb[0] : (b == 1 ? sb[1] : (b == 2 ? sb[2] : sb[3]));
 #pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    const uint4 v = lds128(x + static_cast<uint32_t>(b) * piece_stride + xo[n]);
-                    float d[4];
-                    mma_f16_first(d, a[0], c[0], a[1], c[1], v.x, v.y);
-                    mma_f16(d, a[2], c[2], a[3], c[3], v.z, v.w);
+                for (int j = 0; j < MT; ++j) {
+                    const uint32_t at = (row ^ static_cast<uint32_t>(b * 16)) + j * kStageBytes;
+                    uint32_t a[4], c[4];
+                    e2m1x8_f16(lds32(at), a);
+                    e2m1x8_f16(lds32(at + 512u), c);
+                    const float s0 = b == 0 ? sa[j][0] : (b == 1 ? sa[j][1] : (b == 2 ? sa[j][2] : sa[j][3]));
+                    const float s1 = b == 0 ? sb[j][0] : (b == 1 ? sb[j][1] : (b == 2 ? sb[j][2] : sb[j][3]));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float u = x_unit(field[min(n * 8 + 2 * t + (i & 1), cols - 1)]), s = i < 2 ? s0 : s1;
-                        acc[n][i] = u <= 1.0f ? __fmaf_rn(d[i] * u, s, acc[n][i]) : __fmaf_rn(d[i] * s, u, acc[n][i]);
+                    for (int n = 0; n < N; ++n) {
+                        const uint4 v = lds128(x + static_cast<uint32_t>(b) * piece_stride + xo[n]);
+                        float d[4];
+                        mma_f16_first(d, a[0], c[0], a[1], c[1], v.x, v.y);
+                        mma_f16(d, a[2], c[2], a[3], c[3], v.z, v.w);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float u = x_unit(field[min(n * 8 + 2 * t + (i & 1), cols - 1)]), s = i < 2 ? s0 : s1;
+                            acc[j][n][i] = u <= 1.0f ? __fmaf_rn(d[i] * u, s, acc[j][n][i]) : __fmaf_rn(d[i] * s, u, acc[j][n][i]);
+                        }
                     }
                 }
             }
         }
+    }
+    template <int NT, int N>
+    static __device__ __forceinline__ void consume_shared(const Mat& w, uint32_t slot, int lane, uint32_t key, int step,
+                                                          float (&acc)[NT][4], uint32_t x, uint32_t piece_stride,
+                                                          const uint32_t (&xo)[NT], bool& plain, const uint32_t* field, int cols) {
+        const uint32_t keys[1] = {key};
+        consume_tiles<1, NT, N>(w, slot, lane, keys, step, reinterpret_cast<float(&)[1][NT][4]>(acc), x, piece_stride, xo, plain, field,
+                                cols);
     }
 
     template <int NT>
