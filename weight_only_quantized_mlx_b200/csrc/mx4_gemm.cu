@@ -105,10 +105,10 @@ constexpr uint32_t kAsyncTotal = 227 * 1024 - 512;
 // Shared memory: weight rings | areas | units | sums (S > 1) | steps of X.
 template <int NT>
 struct AsyncSmem {
-    // A warp's tile is MT times 16 rows.  From four column tiles on, two: a piece of
-    // X is read from shared memory once for both, and eight warps have the registers
-    // for their sums (28672 x 8192, 32 rows: 99 -> 91 us, 64 rows: 189 -> 175; at 16
-    // rows 67 -> 66, but 4096 x 4096 13 -> 14).
+    // A warp's tile is MT times 16 rows.  With four column tiles, two: a piece of X is
+    // read from shared memory once for both, and eight warps have the registers for
+    // their sums (28672 x 8192, 32 rows: 99 -> 91 us; at 16 rows 67 -> 66, but 4096 x
+    // 4096 13 -> 14).
     static constexpr int MT = NT <= 2 ? 1 : 2;
     static constexpr int kLogWarps = NT <= 2 ? 4 : 3;
     static constexpr int kWarps = 1 << kLogWarps, kThreads = 32 * kWarps;
@@ -118,8 +118,22 @@ struct AsyncSmem {
     static constexpr uint32_t kAreas = kWarps * kRing;
     static constexpr uint32_t kFields = kAreas + kWarps * kSharedArea;
     static constexpr uint32_t kX = kFields + kMx4GemmMaxM * 4;
-    static_assert(kAsyncTotal - kX - kPartialBytes >= 2u * NT * 8 * 256, "two steps of X");
+    static_assert(kAsyncTotal - kX - kPartialBytes >= 2u * (NT < 4 ? NT * 8 : kMx4GemmMaxM) * 256, "two steps of X");
 };
+
+// Steps of X that fit behind the rest.
+template <int NT>
+__host__ __device__ int x_room(int S, int m) {
+    const int n = static_cast<int>((kAsyncTotal - AsyncSmem<NT>::kX - (S > 1 ? kPartialBytes : 0u)) / (static_cast<uint32_t>(m) * 256u));
+    return n < kMaxXStages ? n : kMaxXStages;
+}
+
+// The steps that a warp takes where 2^i warps share a unit, `join` counted for each join.
+template <int NT>
+__host__ __device__ __forceinline__ int warp_steps(int units, int steps, int i, int join) {
+    const int groups = AsyncSmem<NT>::kWarps >> i;
+    return (units + groups - 1) / groups * (((steps + (1 << i) - 1) >> i) + (i > 0 ? join : 0));
+}
 
 // A block per row of X: its unit (the largest exponent), then its pieces.
 constexpr int kPrepareThreads = 512;
@@ -171,25 +185,26 @@ __global__ void __launch_bounds__(AsyncSmem<NT>::kThreads, 1) k_mx4_gemm_async(c
     const int st0 = static_cast<int>(static_cast<int64_t>(all_steps) * rank / S);
     const int steps = static_cast<int>(static_cast<int64_t>(all_steps) * (rank + 1) / S) - st0;
     constexpr int MT = M::MT, kRows = 16 * MT;
-    const int tiles = (hi - lo + kRows - 1) / kRows;
+    // a unit of work: a tile with one part of up to 8 NT rows of X
+    const int parts = (p.m + 8 * NT - 1) / (8 * NT), units = (hi - lo + kRows - 1) / kRows * parts;
     const uint32_t step_bytes = static_cast<uint32_t>(p.m) * 256u;
     const uint32_t partial = smem_u32(smem) + M::kX, x0 = partial + (S > 1 ? kPartialBytes : 0u);
-    const int room = min(static_cast<int>((smem_u32(smem) + kAsyncTotal - x0) / step_bytes), kMaxXStages);
+    const int room = x_room<NT>(S, p.m);
     uint32_t* field = reinterpret_cast<uint32_t*>(smem + M::kFields);
 
-    // Warps per tile (lane i weighs 2^i of them): steps, and two for a join.  A
-    // stage of X is one step; their number is a multiple of the warps of a tile,
+    // Warps per unit (lane i weighs 2^i of them): steps, and two for a join.  A
+    // stage of X is one step; their number is a multiple of the warps of a unit,
     // so that a warp meets a stage only in its own steps (it could else test the
     // barrier's parity a phase early), and at least twice it.
     int lw;
     {
         const int i = min(lane, M::kLogWarps);
-        int cost = ((tiles + (M::kWarps >> i) - 1) >> (M::kLogWarps - i)) * (((steps + (1 << i) - 1) >> i) + (i > 0 ? 2 : 0));
+        int cost = warp_steps<NT>(units, steps, i, 2);
         if ((2 << i) > room && i > 0) cost = 0x0FFFFFFF;
         lw = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, static_cast<uint32_t>(min(cost, 0x0FFFFFFF)) << 3 | static_cast<uint32_t>(i)) & 7u);
     }
     const int wk = 1 << lw, groups = M::kWarps >> lw, stages = room >> lw << lw;
-    const int rounds = (tiles + groups - 1) / groups;
+    const int rounds = (units + groups - 1) / groups;
     auto full = [&](int s) { return smem_u32(&bars[s]); };
     auto empty = [&](int s) { return smem_u32(&bars[kMaxXStages + s]); };
     if (threadIdx.x == 0) {
@@ -220,18 +235,18 @@ __global__ void __launch_bounds__(AsyncSmem<NT>::kThreads, 1) k_mx4_gemm_async(c
         float4* area = reinterpret_cast<float4*>(smem + M::kAreas + warp * kSharedArea);
         const float4* group_area = reinterpret_cast<const float4*>(smem + M::kAreas + group * wk * kSharedArea);
         constexpr int kAreaVecs = kSharedArea / 16;
-        constexpr int kJoin = NT < 4 ? NT : 4;  // column tiles of a join
+        static_assert(NT * 512 <= kSharedArea, "area");
 
         const int own = kw < steps ? (steps - kw + wk - 1) >> lw : 0;
-        int ptile = own > 0 ? group : tiles, pleft = 0;
+        int punit = own > 0 ? group : units, pleft = 0;
         uint32_t pslot = ring, cslot = ring;
         F::Feed feed[MT];
         auto seek = [&]() {
             pleft = 0;
-            if (ptile < tiles) {
+            if (punit < units) {
 #pragma unroll
                 for (int j = 0; j < MT; ++j) {
-                    const int r = lo + ptile * kRows + 16 * j + g;
+                    const int r = lo + punit / parts * kRows + 16 * j + g;
                     F::start(feed[j], p.w, p.w, r, r + 8, r < hi, r + 8 < hi, lane, st0 + kw);
                 }
                 pleft = own;
@@ -243,7 +258,7 @@ __global__ void __launch_bounds__(AsyncSmem<NT>::kThreads, 1) k_mx4_gemm_async(c
 #pragma unroll
                 for (int j = 0; j < MT; ++j) F::issue(p.w, feed[j], pslot + j * kStageBytes, lane, wk);
                 if (--pleft == 0) {
-                    ptile += groups;
+                    punit += groups;
                     seek();
                 }
             }
@@ -255,13 +270,9 @@ __global__ void __launch_bounds__(AsyncSmem<NT>::kThreads, 1) k_mx4_gemm_async(c
         for (int c = threadIdx.x; c < p.m; c += M::kThreads) field[c] = p.field[c];
         __syncthreads();  // the fields are there
 
-        const int nt = (p.m + 7) / 8;
         const uint32_t piece_stride = static_cast<uint32_t>(p.m) * 64u;
-        uint32_t xo[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) xo[n] = static_cast<uint32_t>(min(n * 8 + g, p.m - 1)) * 64u + static_cast<uint32_t>(t) * 16u;
-        auto store = [&](int r0, int n, int l, const float4& v) {
-            const int r = r0 + (l >> 2), c = n * 8 + 2 * (l & 3), rows = hi - lo;
+        auto store = [&](int r0, int c0, int l, const float4& v) {
+            const int r = r0 + (l >> 2), c = c0 + 2 * (l & 3), rows = hi - lo;
             const float s[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -278,8 +289,12 @@ __global__ void __launch_bounds__(AsyncSmem<NT>::kThreads, 1) k_mx4_gemm_async(c
         uint32_t parity = 0;   // of that stage's use
         const int ahead = (stages - wk) % padded;
         for (int r = 0; r < rounds; ++r) {
-            const int tile = r * groups + group;
-            const bool live = tile < tiles;
+            const int unit = r * groups + group, tile = unit / parts, c0 = (unit - tile * parts) * 8 * NT;
+            const bool live = unit < units;
+            const int cols = p.m - c0, nt = (cols + 7) / 8;  // column tiles; the kernel's others repeat the last row of X
+            uint32_t xo[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) xo[n] = static_cast<uint32_t>(min(c0 + n * 8 + g, p.m - 1)) * 64u + static_cast<uint32_t>(t) * 16u;
             float acc[MT][NT][4];
             uint32_t key[MT];
 #pragma unroll
@@ -308,8 +323,12 @@ __global__ void __launch_bounds__(AsyncSmem<NT>::kThreads, 1) k_mx4_gemm_async(c
                     cp_async_wait<M::kDepth - 2>();
                     __syncwarp();  // the copies of all lanes have landed; the slot refilled below is read out
                     issue();
-                    F::consume_tiles<MT, NT, NT>(p.w, cslot, lane, key, st0 + k, acc, x0 + static_cast<uint32_t>(stage) * step_bytes,
-                                                piece_stride, xo, plain, field, p.m);
+                    if (NT == 4 && nt <= 2)
+                        F::consume_tiles<MT, NT, (NT + 1) / 2>(p.w, cslot, lane, key, st0 + k, acc, x0 + static_cast<uint32_t>(stage) * step_bytes,
+                                                    piece_stride, xo, plain, field + c0, cols);
+                    else
+                        F::consume_tiles<MT, NT, NT>(p.w, cslot, lane, key, st0 + k, acc, x0 + static_cast<uint32_t>(stage) * step_bytes,
+                                                    piece_stride, xo, plain, field + c0, cols);
                     cslot = cslot == ring + M::kRing - M::kStage ? ring : cslot + M::kStage;
                 }
                 __syncwarp();
@@ -324,34 +343,29 @@ __global__ void __launch_bounds__(AsyncSmem<NT>::kThreads, 1) k_mx4_gemm_async(c
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
                 const int r0 = tile * kRows + 16 * j;
-                if (plain) F::to_numbers<NT>(acc[j], field, p.m, t);
+                if (plain) F::to_numbers<NT>(acc[j], field + c0, cols, t);
+                if (wk == 1) {
 #pragma unroll
-                for (int n0 = 0; n0 < NT; n0 += kJoin) {
-                    if (n0 >= nt) break;
-                    if (wk == 1) {
-#pragma unroll
-                        for (int n = n0; n < n0 + kJoin; ++n)
-                            if (n < nt) store(r0, n, lane, make_float4(acc[j][n][0], acc[j][n][1], acc[j][n][2], acc[j][n][3]));
-                        continue;
-                    }
-#pragma unroll
-                    for (int n = 0; n < kJoin; ++n)
-                        area[n * 32 + lane] = make_float4(acc[j][n0 + n][0], acc[j][n0 + n][1], acc[j][n0 + n][2], acc[j][n0 + n][3]);
-                    group_sync(group, wk);
-                    for (int i = kw * 32 + lane; i < kJoin * 32; i += wk * 32) {
-                        if (n0 + (i >> 5) >= nt) continue;
-                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int w = 0; w < wk; ++w) {
-                            const float4 q = group_area[w * kAreaVecs + i];
-                            v.x += q.x;
-                            v.y += q.y;
-                            v.z += q.z;
-                            v.w += q.w;
-                        }
-                        store(r0, n0 + (i >> 5), i & 31, v);
-                    }
-                    group_sync(group, wk);
+                    for (int n = 0; n < NT; ++n)
+                        if (n < nt) store(r0, c0 + n * 8, lane, make_float4(acc[j][n][0], acc[j][n][1], acc[j][n][2], acc[j][n][3]));
+                    continue;
                 }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) area[n * 32 + lane] = make_float4(acc[j][n][0], acc[j][n][1], acc[j][n][2], acc[j][n][3]);
+                group_sync(group, wk);
+                for (int i = kw * 32 + lane; i < NT * 32; i += wk * 32) {
+                    if (i >> 5 >= nt) continue;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int w = 0; w < wk; ++w) {
+                        const float4 q = group_area[w * kAreaVecs + i];
+                        v.x += q.x;
+                        v.y += q.y;
+                        v.z += q.z;
+                        v.w += q.w;
+                    }
+                    store(r0, c0 + (i >> 5) * 8, i & 31, v);
+                }
+                group_sync(group, wk);
             }
         }
         cp_async_wait<0>();
@@ -421,7 +435,7 @@ cudaError_t launch_async(AsyncParams p, cudaStream_t stream) {
     // 18.5 us, 1 23.6), 4096 x 14336 (S = 4 51 us, 2 63, 1 60) and 4096 x 4096 (S = 1
     // 24.2 us, 4 24.8).
     const int steps = (p.K + Mx4HalfFmt::kStepCols - 1) / Mx4HalfFmt::kStepCols;
-    const int per_step = NT == 1 ? 80 : (NT == 2 ? 130 : (NT == 4 ? 340 : 700));
+    const int per_step = NT == 1 ? 81 : (NT == 2 ? 107 : 300);
     int64_t best = INT64_MAX;
     unsigned grid = 1;
     for (int S = 1; S <= 8 && S <= steps; S *= 2) {
@@ -433,11 +447,16 @@ cudaError_t launch_async(AsyncParams p, cudaStream_t stream) {
         const int64_t rows = (p.N + clusters - 1) / clusters;
         if (S > 1 && (rows + 1) * p.m * 4 > kPartialBytes) continue;
         constexpr int kRows = 16 * AsyncSmem<NT>::MT;
-        const int64_t own = (steps + S - 1) / S, tiles = (rows + kRows - 1) / kRows;
-        int64_t cost = tiles * own * per_step;
+        const int64_t own = (steps + S - 1) / S, units = (rows + kRows - 1) / kRows * ((p.m + 8 * NT - 1) / (8 * NT));
+        int64_t cost = INT64_MAX;
+        for (int i = 0; i <= AsyncSmem<NT>::kLogWarps && (i == 0 || (2 << i) <= x_room<NT>(S, p.m)); ++i) {
+            const int64_t c = static_cast<int64_t>(warp_steps<NT>(static_cast<int>(units), static_cast<int>(own), i, 1)) *
+                              AsyncSmem<NT>::kWarps * per_step;
+            if (c < cost) cost = c;
+        }
         if (rows * own * 3 > cost) cost = rows * own * 3;
         cost += p.m * own * 6;
-        if (S > 1) cost += 3000 + rows * p.m;
+        if (S > 1) cost += 5000 + rows * p.m;
         if (cost < best) {
             best = cost;
             p.S = S;
@@ -475,7 +494,7 @@ cudaError_t launch_prepared(const Mx4View& w, const void* x, void* y, int m, cud
                    steps, xp, field);
     if (e == cudaSuccess)
         e = m <= 8 ? launch_async<1>(p, stream)
-                   : (m <= 16 ? launch_async<2>(p, stream) : (m <= 32 ? launch_async<4>(p, stream) : launch_async<8>(p, stream)));
+                   : (m <= 16 ? launch_async<2>(p, stream) : launch_async<4>(p, stream));
     const cudaError_t ef = cudaFreeAsync(ws, stream);
     return e != cudaSuccess ? e : ef;
 }
