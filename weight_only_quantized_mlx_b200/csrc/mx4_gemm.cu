@@ -1,19 +1,25 @@
 // Y = X W^T with an MX4 weight and BF16 activations, up to 64 rows of X.
 //
-// HBM-bound on the weight (17/32 bytes per element): blocks stream balanced
-// ranges of its rows, every byte once (row_stream.cuh).  One rounding, of the
-// result.
+// Blocks stream balanced ranges of the weight's rows (17/32 bytes per element), every
+// byte once (row_stream.cuh).  One rounding, of the result.
 //
-// k_mx4_gemm, up to 8 rows of X: a block keeps them in shared memory,
-// converted on the way (in chunks of K where they do not fit).
+// k_mx4_gemm, up to 8 rows of X: a block keeps them in shared memory, converted on
+// the way (in chunks of K where they do not fit).  28672 x 8192, one row: 39 us, 3.2
+// TB/s of the weight, half of the measured copy rate; the warps' instructions bound
+// it (issue slots 64 % filled; turning codes into FP16 alone takes about half the
+// time that the weight needs from HBM).  4096 x 4096: 7.3 us, mostly the latencies of
+// one launch, of the first loads and of the join.
 //
 // k_mx4_gemm_async, more rows: every block needs all of X over its columns, and
 // fetching and converting them between products took most of the time (4096 x
 // 4096, m = 64: 80 us).  So k_mx4_prepare writes X once in the order and units in
 // which the products take it, step after step, and bulk copies bring the steps into
-// a ring while the warps multiply.  S blocks of a
-// cluster share a range of rows and split K, which divides the copies of X by S,
-// and add their sums through distributed shared memory in rank order.
+// a ring while the warps multiply.  Where rows are few, four blocks of a cluster share
+// a range of rows and split K, which divides the copies of X, and add their sums
+// through distributed shared memory in rank order.  28672 x 8192: 16 rows 67 us, 32
+// rows 92, 64 rows 171; 4096 x 4096: 14, 16, 19.  The products bound it (without
+// them 33 us whatever the rows at 28672 x 8192; without the copies of the weight 64,
+// 93 and 145).
 #include <cooperative_groups.h>
 
 #include "row_stream.cuh"
@@ -100,6 +106,7 @@ struct AsyncParams {
 
 constexpr uint32_t kPartialBytes = 32 * 1024;  // S > 1: fp32 sums of a cluster's rows
 constexpr int kMaxXStages = 16;
+constexpr int kSplit = 4;  // blocks of a cluster that split K, where they do
 constexpr uint32_t kAsyncTotal = 227 * 1024 - 512;
 
 // Shared memory: weight rings | areas | units | sums (S > 1) | steps of X.
@@ -379,14 +386,12 @@ __global__ void __launch_bounds__(AsyncSmem<NT>::kThreads, 1) k_mx4_gemm_async(c
         cluster.sync();  // all sums are there
         const int rows = hi - lo, n = rows * p.m;
         for (int i = rank * static_cast<int>(blockDim.x) + threadIdx.x; i < n; i += S * static_cast<int>(blockDim.x)) {
-            float v[8];  // all ranks' sums, in flight together
+            float v[kSplit];  // all ranks' sums, in flight together
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (q < S) v[q] = ld_cluster_f32(partial + static_cast<uint32_t>(i) * 4u, static_cast<uint32_t>(q));
+            for (int q = 0; q < kSplit; ++q) v[q] = ld_cluster_f32(partial + static_cast<uint32_t>(i) * 4u, static_cast<uint32_t>(q));
             float s = v[0];
 #pragma unroll
-            for (int q = 1; q < 8; ++q)
-                if (q < S) s += v[q];
+            for (int q = 1; q < kSplit; ++q) s += v[q];
             const int c = i / rows, row = i - c * rows;
             p.y[static_cast<int64_t>(c) * p.N + lo + row] = static_cast<uint16_t>(pack_bf16x2(s, 0.f));
         }
@@ -394,19 +399,18 @@ __global__ void __launch_bounds__(AsyncSmem<NT>::kThreads, 1) k_mx4_gemm_async(c
     }
 }
 
-// Clusters of S blocks that the device holds at once (asked once per device).
+// Clusters of kSplit blocks that the device holds at once (asked once per device).
 template <int NT>
-int resident_clusters(cudaLaunchConfig_t& cfg, int S) {
-    static std::atomic<int> known[64][4];
-    const int dev = device_info().device, slot = S == 8 ? 3 : (S == 4 ? 2 : S - 1);
-    int n = known[dev][slot].load(std::memory_order_relaxed);
+int resident_clusters(const cudaLaunchConfig_t& cfg) {
+    static std::atomic<int> known[64];
+    const int dev = device_info().device;
+    int n = known[dev].load(std::memory_order_relaxed);
     if (n == 0) {
-        if (S == 1) n = device_info().sm_count;
-        else if (cudaOccupancyMaxActiveClusters(&n, k_mx4_gemm_async<NT>, &cfg) != cudaSuccess || n < 1) {
+        if (cudaOccupancyMaxActiveClusters(&n, k_mx4_gemm_async<NT>, &cfg) != cudaSuccess || n < 1) {
             (void)cudaGetLastError();
-            n = device_info().sm_count / S / 2 > 0 ? device_info().sm_count / S / 2 : 1;
+            n = device_info().sm_count / kSplit / 2 > 0 ? device_info().sm_count / kSplit / 2 : 1;
         }
-        known[dev][slot].store(n, std::memory_order_relaxed);
+        known[dev].store(n, std::memory_order_relaxed);
     }
     return n;
 }
@@ -428,21 +432,20 @@ cudaError_t launch_async(AsyncParams p, cudaStream_t stream) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
 
-    // S: the one that ends first by a model in cycles of an SM - the products of a
-    // tile's steps (measured at 28672 x 8192) or the weight at its share of HBM, the
-    // copies of X at some 25 bytes a cycle, about half of them hidden, and the
-    // exchange of sums.  It picks what measured best at 1024 x 4096 (64 rows: S = 8
-    // 18.5 us, 1 23.6), 4096 x 14336 (S = 4 51 us, 2 63, 1 60) and 4096 x 4096 (S = 1
-    // 24.2 us, 4 24.8).
+    // S: 1 or kSplit, the one that ends first by a model in cycles of an SM: the
+    // products of its warps (measured at 28672 x 8192) or the weight at its share of
+    // HBM; what is not hidden of the copies of X; and the exchange of sums.  Measured
+    // with 64 rows at S = 1, 2, 4 and 8: 1024 x 4096 19.0, 16.9, 13.8, 15.1 us; 4096 x
+    // 4096 19.4, 21.4, 22.3, -; 8192 x 28672 153, 163, -, - (- : too many sums).
     const int steps = (p.K + Mx4HalfFmt::kStepCols - 1) / Mx4HalfFmt::kStepCols;
     const int per_step = NT == 1 ? 81 : (NT == 2 ? 107 : 300);
     int64_t best = INT64_MAX;
     unsigned grid = 1;
-    for (int S = 1; S <= 8 && S <= steps; S *= 2) {
+    for (int S = 1; S <= kSplit && S <= steps; S *= kSplit) {
         cfg.gridDim = dim3(static_cast<unsigned>(S));
         attr[0].val.clusterDim.x = static_cast<unsigned>(S);
         cfg.numAttrs = 1;
-        int clusters = resident_clusters<NT>(cfg, S);
+        int clusters = S == 1 ? device_info().sm_count : resident_clusters<NT>(cfg);
         if (clusters > (p.N + 7) / 8) clusters = (p.N + 7) / 8;
         const int64_t rows = (p.N + clusters - 1) / clusters;
         if (S > 1 && (rows + 1) * p.m * 4 > kPartialBytes) continue;
@@ -455,8 +458,8 @@ cudaError_t launch_async(AsyncParams p, cudaStream_t stream) {
             if (c < cost) cost = c;
         }
         if (rows * own * 3 > cost) cost = rows * own * 3;
-        cost += p.m * own * 6;
-        if (S > 1) cost += 5000 + rows * p.m;
+        cost += p.m * own * 3 / 2;
+        if (S > 1) cost += cost / 32 + 4000 + rows * p.m;
         if (cost < best) {
             best = cost;
             p.S = S;
