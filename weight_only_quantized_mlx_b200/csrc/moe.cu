@@ -12,9 +12,16 @@
 // experts' gate and up rows (row_stream.cuh; the 16 rows of a tile are 8 gate
 // rows and the same 8 up rows, so silu(gate) * up is a lane's own business),
 // writes h, crosses a grid barrier, and streams its share of the down rows over
-// all experts at once.  HBM-bound on the experts hit; each weight byte is read
-// once whatever the number of tokens.  The ring is filled with down rows
+// all experts at once.  Each weight byte of a hit expert is read once (again for every
+// 8 NT tokens more of one expert).  The ring is filled with down rows
 // before the barrier, so the barrier's wait overlaps their copies.
+//
+// Measured: one token, two of 8 experts of 4096 x 14336, 8 bits: 107 us (the
+// weights' copy time is 57); 64 tokens, 128 experts of 4128 x 1504, MX4: 485 us
+// (190).  The warps' instructions bound both (issue slots 63 % filled), most of them
+// for turning codes into operands.  One token, 8 of 64 experts of 2048 x 1024, MX4:
+// 25 us (4), a chain of latencies: router 5 us, lists 1.4, first copies and
+// activations 2.3, gate and up 5, barrier 3.5, down 4.2.
 //
 // Rounding: h is rounded to BF16 once (with p in it), the operand type of the
 // tensor pipe; sums, silu and p are fp32.

@@ -26,6 +26,11 @@
 // room for scales.  Columns behind K and rows behind the operands read as zero
 // codes under scale 1.
 //
+// Measured: 8192 x 14336 x 4096 233 us (4.1 PFLOP/s), 8192 x 4096 x 14336 200 us (4.8),
+// 509 x 4100 x 14368 38 us (1.6), 64 x 4096 x 14336 16 us.  A k-block takes 0.9 us at
+// 224 rows where its MMAs alone take about half: codes and scales must have landed,
+// and the scales be in TMEM, before the first MMA.
+//
 // All waits are bounded; after one gives up the producers and the MMA thread
 // issue nothing more and wait (bounded) for what they issued.
 #include <cooperative_groups.h>
