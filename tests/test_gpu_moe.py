@@ -276,3 +276,76 @@ def test_quantized_experts_as_a_program_makes_them():
     xb = synth.activations(g, m, H)
     want, _, err = L.reference(xb, k)
     check(L.run(dev(xb), k), want, err)
+
+
+def test_equal_tokens_of_many_experts_take_several_entries():
+    """Few tokens an expert on average, all 64 on the same sixteen: each expert's weights are streamed several times."""
+    L = Layer(21, 256, 128, 64, 0)
+    xb = np.repeat(synth.activations(L.g, 1, 128), 64, axis=0)
+    want, _, err = L.reference(xb[:1], 16)
+    y = L.run(dev(xb), 16)
+    assert torch.equal(y, y[:1].expand_as(y))
+    check(y[:1], want, err)
+
+
+@pytest.mark.parametrize("m", [2, 11])
+@pytest.mark.parametrize("group", [64, 0], ids=["gs64", "mx4"])
+def test_offsets_past_32_bits(m, group):
+    """Experts of more than 2^32 bytes of codes per matrix, the last one chosen."""
+    E, I, H = 256, 1024, 16512 if group else 33024
+    g = torch.Generator("cuda").manual_seed(22)
+    handles, values, keep = [], [], []
+    for rows, cols in ((E * I, H), (E * I, H), (E * H, I)):
+        last = slice(rows - rows // E, rows)
+        if group:
+            assert rows * cols > 2 ** 32
+            p = torch.randint(-2 ** 31, 2 ** 31 - 1, (rows, cols // 4), dtype=torch.int32, device="cuda", generator=g)
+            s = torch.full((rows, cols // group), 2.0 ** -7 / math.sqrt(cols), dtype=torch.bfloat16, device="cuda")
+            b = torch.full_like(s, -1.0 / math.sqrt(cols))
+            keep.append((p, s, b))
+            handles.append(mq.weight_view(p, s, b, group))
+            q = p[last].contiguous().view(torch.uint8).double().reshape(-1, cols // group, group)
+            v = (s[last].double()[:, :, None] * q + b[last].double()[:, :, None]).float().bfloat16().double()
+        else:
+            assert rows * cols // 2 > 2 ** 32
+            codes = torch.randint(-2 ** 31, 2 ** 31 - 1, (rows, cols // 8), dtype=torch.int32, device="cuda", generator=g)
+            e = 127 + round(math.log2(1 / (2.9 * math.sqrt(cols))))
+            scales = torch.randint(e - 1, e + 2, (rows, cols // 32), dtype=torch.uint8, device="cuda", generator=g)
+            handles.append(mq.mx4_view(codes, scales))
+            grid = torch.tensor(np.concatenate([ref.GRID, -ref.GRID]), device="cuda")
+            c = torch.stack([(codes[last] >> (4 * i)) & 15 for i in range(8)], dim=-1).reshape(-1, cols // 32, 32)
+            v = grid[c.long()] * torch.exp2(scales[last].double() - 127)[:, :, None]
+        values.append(v.reshape(1, rows // E, cols))
+    xb = synth.activations(synth.rng(22), m, H)
+    x = dev(xb)
+    router = torch.zeros(E, H, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty(m, H, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(mq.mlxq_moe_workspace_bytes(H, I, 1, m), dtype=torch.uint8, device="cuda")
+    call = mq.mlxq_moe if group else mq.mlxq_mx4_moe
+    for t in range(m):  # a row of the router that every token's logit is largest with: one token at a time
+        router[E - 1] = x[t]
+        call(router, *handles, E, 1, x[t:t + 1], y[t:t + 1], 1, ws)
+    want, _, err = ref.moe(f64(xb), torch.ones(1, H, dtype=torch.float64, device="cuda"), *values, 1, True)
+    check(y, want, err)
+    both = torch.empty_like(y)  # all tokens in one call: those that the last row draws there get the same expert
+    router[E - 1] = x.float().mean(dim=0).bfloat16()
+    call(router, *handles, E, 1, x, both, m, ws)
+    drawn = (x.double() @ router[E - 1].double()) > 0.01
+    assert bool(drawn.any())
+    check(both[drawn], want[drawn], err[drawn])
+
+
+@pytest.mark.parametrize("group", [64, 0], ids=["gs64", "mx4"])
+def test_layers_on_two_streams_at_once(group):
+    """Calls on two streams, a workspace each; and other small sizes in between on a third."""
+    L = Layer(23, 16, 1024, 256, group)
+    xs = [dev(synth.activations(L.g, m, 1024)) for m in (1, 40, 8)]
+    want = [L.run(x, 4) for x in xs]
+    ys, wss = [torch.zeros_like(w) for w in want], [L.workspace(4, x.shape[0]) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(20):
+        for x, y, ws, s in zip(xs, ys, wss, streams):
+            L.run(x, 4, ws=ws, y=y, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, w) for y, w in zip(ys, want))

@@ -410,3 +410,86 @@ def test_quantize_then_matmul_in_a_graph():
     wv, av = ref.values(*ref.quantize(wb)), ref.values(*ref.quantize(xb))
     want = av @ wv.T
     assert np.all(np.abs(bits_to_f64(host_bits(y)) - want) <= bound(np.abs(wv), np.abs(av), want, K))
+
+
+def big(rows, cols, seed):
+    """A handle over more than 2^32 bytes of random codes; scales near 2^-7."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    codes = torch.randint(-2 ** 31, 2 ** 31 - 1, (rows, cols // 8), dtype=torch.int32, device="cuda", generator=g)
+    scales = torch.randint(118, 123, (rows, cols // 32), dtype=torch.uint8, device="cuda", generator=g)
+    return mq.mx4_view(codes, scales)
+
+
+def rows_of(h, lo, hi):
+    """fp64 values of rows [lo, hi)."""
+    codes = h.tensors[0][lo:hi].cpu().numpy().view(np.uint32)
+    c = ((codes[:, :, None] >> (4 * np.arange(8, dtype=np.uint32))) & 15).astype(np.uint8).reshape(hi - lo, -1)
+    return ref.values(c, h.tensors[1][lo:hi].cpu().numpy())
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 bytes of codes, and more than 2^32 elements on the BF16 side: first, middle and last rows."""
+    N, K = 530000, 16416
+    assert N * K // 2 > 2 ** 32
+    h = big(N, K, 20)
+    g = synth.rng(20)
+    spans = [(0, 20), (N * 2 // 3, N * 2 // 3 + 20), (N - 37, N)]
+    for m in (2, 20):
+        xb = synth.activations(g, m, K)
+        x = bits_to_f64(xb)
+        y = torch.empty(m, N, dtype=torch.bfloat16, device="cuda")
+        mq.mlxq_mx4_gemm(h, dev(xb), y, m)
+        for lo, hi in spans:
+            w = rows_of(h, lo, hi)
+            want = x @ w.T
+            err = np.abs(bits_to_f64(host_bits(y[:, lo:hi].contiguous())) - want)
+            assert np.all(err <= bound(np.abs(w), np.abs(x), want, K))
+    out = torch.empty(N, K, dtype=torch.bfloat16, device="cuda")
+    mq.mlxq_mx4_dequant(h, out)
+    for lo, hi in spans:
+        assert np.array_equal(bits_to_f64(host_bits(out[lo:hi])), rows_of(h, lo, hi))
+    back = mq.mx4_empty(N, K)
+    mq.mlxq_mx4_quantize(out, back)
+    again = torch.empty_like(out)
+    mq.mlxq_mx4_dequant(back, again)
+    assert torch.equal(out, again)  # the values of a block and its largest binade come back
+    del out, again, back
+    # Y of more than 2^32 elements
+    M, N, K = 66000, 66000, 64
+    a, w = big(M, K, 21), big(N, K, 22)
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    mq.mlxq_mx4_matmul(w, a, y)
+    for i in (0, M - 30):
+        for j in (0, N - 40):
+            va, vw = rows_of(a, i, i + 30), rows_of(w, j, j + 40)
+            want = va @ vw.T
+            err = np.abs(bits_to_f64(host_bits(y[i:i + 30, j:j + 40].contiguous())) - want)
+            assert np.all(err <= bound(np.abs(vw), np.abs(va), want, K))
+
+
+def test_calls_on_two_streams_at_once():
+    """Each call again and again on two streams, other operands on each: the bits of one call alone."""
+    jobs = []
+    for seed, (m, N, K) in enumerate([(20, 700, 14336), (9, 4100, 4096), (64, 1024, 4128), (3, 3000, 2048)]):
+        g, codes, scales, h = make(30 + seed, N, K)
+        x = dev(synth.activations(g, m, K))
+        a = mq.mx4_empty(m, K)
+        jobs.append((h, x, a, m, N))
+
+    def run(job, stream=None):
+        h, x, a, m, N = job
+        y, z = (torch.full((m, N), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        mq.mlxq_mx4_gemm(h, x, y, m, stream)
+        mq.mlxq_mx4_quantize(x, a, stream)
+        mq.mlxq_mx4_matmul(h, a, z, stream)
+        return y, z
+
+    want = [run(j) for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        got = [run(j, streams[i % 2]) for i, j in enumerate(jobs)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for a, b in zip(got, want) for p, q in zip(a, b))
