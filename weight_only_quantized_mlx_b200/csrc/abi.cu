@@ -490,6 +490,7 @@ const DeviceInfo& device_info() {
     if (g_dev_ready[dev].load(std::memory_order_acquire)) return g_dev[dev];
     std::lock_guard<std::mutex> lk(g_dev_mu);
     if (!g_dev_ready[dev].load(std::memory_order_relaxed)) {
+        SetupScope scope;
         DeviceInfo di{};
         di.device = dev;
         cudaDeviceGetAttribute(&di.sm_count, cudaDevAttrMultiProcessorCount, dev);

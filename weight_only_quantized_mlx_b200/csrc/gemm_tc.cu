@@ -564,6 +564,7 @@ cudaError_t workspace_pool(int device, cudaMemPool_t* out) {
     if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (!made[device]) {
+        SetupScope scope;
         cudaMemPoolProps props{};
         props.allocType = cudaMemAllocationTypePinned;
         props.handleTypes = cudaMemHandleTypeNone;

@@ -42,6 +42,17 @@ const DeviceInfo& device_info();
 // Address of the library's device status word on the current device.
 unsigned int* device_status_ptr();
 
+// What a first call on a device sets up (attributes, the pool, occupancy) may come
+// while a stream is being captured; in a capture's default mode such calls would be
+// refused and end it.  None of them touches a stream.
+struct SetupScope {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    SetupScope() { (void)cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~SetupScope() { (void)cudaThreadExchangeStreamCaptureMode(&mode); }
+    SetupScope(const SetupScope&) = delete;
+    SetupScope& operator=(const SetupScope&) = delete;
+};
+
 // Raise a kernel's dynamic shared-memory limit to `bytes` once per device
 // (cudaFuncSetAttribute is a host round trip; launches then skip it).
 // `configured` is the calling launch site's own per-device record (one static
@@ -51,6 +62,7 @@ cudaError_t ensure_dynamic_smem(Kernel kern, size_t bytes, std::atomic<int> (&co
     const int dev = device_info().device;
     const int want = static_cast<int>(bytes);
     if (configured[dev].load(std::memory_order_relaxed) >= want) return cudaSuccess;
+    SetupScope scope;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, want);
     if (e == cudaSuccess) {
         int cur = configured[dev].load(std::memory_order_relaxed);

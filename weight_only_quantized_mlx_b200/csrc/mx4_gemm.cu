@@ -406,6 +406,7 @@ int resident_clusters(const cudaLaunchConfig_t& cfg) {
     const int dev = device_info().device;
     int n = known[dev].load(std::memory_order_relaxed);
     if (n == 0) {
+        SetupScope scope;
         if (cudaOccupancyMaxActiveClusters(&n, k_mx4_gemm_async<NT>, &cfg) != cudaSuccess || n < 1) {
             (void)cudaGetLastError();
             n = device_info().sm_count / kSplit / 2 > 0 ? device_info().sm_count / kSplit / 2 : 1;
