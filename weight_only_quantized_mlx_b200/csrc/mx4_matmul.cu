@@ -12,7 +12,9 @@
 //               (tcgen05.cp) and issues the MMAs
 //   warps 2, 3 and 12, 13  scales of the weight rows and of the activation rows,
 //               128 rows each: 8 bytes a row and k-block, loaded two k-blocks
-//               ahead, put into the 128 x 4 order that tcgen05.cp and
+//               ahead (16 bytes for two of them where alignment allows: a row's
+//               sector is then fetched half as often), put into the 128 x 4
+//               order that tcgen05.cp and
 //               the MMA expect (row r, group g of a set of four: byte
 //               (r % 32) 16 + (r / 32) 4 + g)
 //   warps 4-11  read the accumulators (tcgen05.ld) as BF16 into registers,
@@ -26,10 +28,11 @@
 // room for scales.  Columns behind K and rows behind the operands read as zero
 // codes under scale 1.
 //
-// Measured: 8192 x 14336 x 4096 233 us (4.1 PFLOP/s), 8192 x 4096 x 14336 200 us (4.8),
-// 509 x 4100 x 14368 38 us (1.6), 64 x 4096 x 14336 16 us.  A k-block takes 0.9 us at
-// 224 rows where its MMAs alone take about half: codes and scales must have landed,
-// and the scales be in TMEM, before the first MMA.
+// Measured: 8192 x 14336 x 4096 222 us (4.3 PFLOP/s), 8192 x 4096 x 14336 200 us (4.8),
+// 509 x 4100 x 14368 38 us (1.6), 64 x 4096 x 14336 16 us.  With parts cut out (the
+// first two and the third, when they took 235, 202 and 38 us): no loads of scales 205,
+// 182, 30; no copies of scales to TMEM 231, 190, 37; neither 186, 162, 29; no codes
+// 198, 175, 35; MMAs alone 151, 129, 24.
 //
 // All waits are bounded; after one gives up the producers and the MMA thread
 // issue nothing more and wait (bounded) for what they issued.
@@ -109,9 +112,11 @@ __device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
 
 // The eight scale bytes of one row and k-block, from the table's byte e on: words
 // now, bytes when they are due, so that the loads of many rows are in flight
-// together.  WIDE: rows are multiples of 8 bytes and the table is 8-byte aligned.
-// Otherwise the bytes start anywhere in a word; words that the table does not
-// have all of are not read.
+// together.  SCALES_PAIR: rows are multiples of 16 bytes, the table is 16-byte
+// aligned and the k-blocks come in pairs, which share a load.  SCALES_WIDE:
+// 8 bytes.  SCALES_ANY: the bytes start anywhere in a word; words that the table does
+// not have all of are not read.
+enum ScaleLoads { SCALES_ANY, SCALES_WIDE, SCALES_PAIR };
 __device__ __forceinline__ uint32_t ldg_if(const uint8_t* p, bool read) {
     uint32_t v;
     asm volatile(
@@ -123,27 +128,33 @@ __device__ __forceinline__ uint32_t ldg_if(const uint8_t* p, bool read) {
         : "l"(p), "r"(static_cast<uint32_t>(read)));
     return v;
 }
-template <bool WIDE>
-__device__ __forceinline__ void load_words(uint32_t (&w)[WIDE ? 2 : 3], const uint8_t* scales, int64_t e, int64_t table, bool live) {
-    if (WIDE) {
+template <ScaleLoads LOADS>
+constexpr int kScaleWords = LOADS == SCALES_ANY ? 3 : (LOADS == SCALES_WIDE ? 2 : 4);
+template <ScaleLoads LOADS>
+__device__ __forceinline__ void load_words(uint32_t (&w)[kScaleWords<LOADS>], const uint8_t* scales, int64_t e, int64_t table, bool live) {
+    if constexpr (LOADS == SCALES_PAIR) {
+        uint4 v = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        if (live) v = __ldg(reinterpret_cast<const uint4*>(scales + e));
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    } else if constexpr (LOADS == SCALES_WIDE) {
         uint2 v = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
         if (live) v = __ldg(reinterpret_cast<const uint2*>(scales + e));
         w[0] = v.x;
         w[1] = v.y;
-        return;
-    }
-    const int64_t at = e & ~int64_t{3};
+    } else {
+        const int64_t at = e & ~int64_t{3};
 #pragma unroll
-    for (int i = 0; i < 3; ++i) w[i] = ldg_if(scales + at + 4 * i, live && at + 4 * i + 4 <= table);
+        for (int i = 0; i < 3; ++i) w[i] = ldg_if(scales + at + 4 * i, live && at + 4 * i + 4 <= table);
+    }
 }
 // `left`: blocks left in the row; behind them, and where there is no row, 127 (scale 1).
-template <bool WIDE>
-__device__ __forceinline__ uint2 scale_bytes(const uint32_t (&w)[WIDE ? 2 : 3], const uint8_t* scales, int64_t e, int64_t table, bool live,
-                                             int left) {
-    if (WIDE) return make_uint2(w[0], w[1]);
+__device__ __forceinline__ uint2 scale_bytes(const uint32_t (&w)[3], const uint8_t* scales, int64_t e, int64_t table, bool live, int left) {
     if (!live) return make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
     const uint32_t sh = 8u * static_cast<uint32_t>(e & 3);
-    uint32_t lo = __funnelshift_r(w[0], w[1], sh), hi = __funnelshift_r(w[1], w[WIDE ? 1 : 2], sh);
+    uint32_t lo = __funnelshift_r(w[0], w[1], sh), hi = __funnelshift_r(w[1], w[2], sh);
     if (e + 8 > (table & ~int64_t{3})) {  // the table's last bytes, not a whole word
         lo = hi = 0;
         for (int i = 0; i < 4; ++i) {
@@ -156,7 +167,7 @@ __device__ __forceinline__ uint2 scale_bytes(const uint32_t (&w)[WIDE ? 2 : 3], 
     return make_uint2((lo & k0) | (0x7F7F7F7Fu & ~k0), (hi & k1) | (0x7F7F7F7Fu & ~k1));
 }
 
-template <bool WIDE>
+template <ScaleLoads LOADS>
 __global__ void __launch_bounds__(kThreads, 1)
     k_mx4_matmul(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const MatmulParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -278,44 +289,58 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint8_t* scales = weight ? p.w_scales : p.a_scales;
         const int rows = weight ? p.N : p.m, span = weight ? kBM : p.BN;
         const int64_t table = static_cast<int64_t>(rows) * p.G;
-        constexpr int kWords = WIDE ? 2 : 3;
+        constexpr int kWords = kScaleWords<LOADS>;
+        constexpr int kAhead = LOADS == SCALES_PAIR ? 2 : 1;  // k-blocks of a load
         auto first_row = [&](int tile) { return weight ? (tile % tiles_n) * kBM : (tile / tiles_n) * p.BN; };
         auto load = [&](uint32_t (&v)[4][kWords], int tile, int kb) {
             const int r0 = first_row(tile);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = half * 128 + lane + 32 * i;
-                load_words<WIDE>(v[i], scales, static_cast<int64_t>(r0 + r) * p.G + (kb0 + kb) * 8, table, r < span && r0 + r < rows);
+                load_words<LOADS>(v[i], scales, static_cast<int64_t>(r0 + r) * p.G + (kb0 + kb) * 8, table, r < span && r0 + r < rows);
             }
         };
         bool ok = true;
         int it = 0, ltile = first, lkb = 0;  // what is loaded next
         uint32_t v[2][4][kWords];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (ltile < tiles) load(v[i], ltile, lkb);
-            if (++lkb == num_kb) {
+        auto load_next = [&](uint32_t (&d)[4][kWords]) {
+            if (ltile < tiles) load(d, ltile, lkb);
+            if ((lkb += kAhead) >= num_kb) {
                 lkb = 0;
                 ltile += stride;
             }
-        }
+        };
+        if (LOADS != SCALES_PAIR) load_next(v[0]);
+        load_next(v[1]);
         for (int tile = first; tile < tiles && ok; tile += stride) {
             const int r0 = first_row(tile);
             for (int kb = 0; kb < num_kb; ++kb, ++it) {
                 const int s = it % kStages;
                 uint2 c[4];
+                auto advance = [&]() {  // the loaded words are due, others take their place
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = half * 128 + lane + 32 * i;
-                    c[i] = scale_bytes<WIDE>(v[0][i], scales, static_cast<int64_t>(r0 + r) * p.G + (kb0 + kb) * 8, table,
-                                             r < span && r0 + r < rows, p.G - (kb0 + kb) * 8);
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < kWords; ++j) v[0][i][j] = v[1][i][j];
-                }
-                if (ltile < tiles) load(v[1], ltile, lkb);
-                if (++lkb == num_kb) {
-                    lkb = 0;
-                    ltile += stride;
+                        for (int j = 0; j < kWords; ++j) v[0][i][j] = v[1][i][j];
+                    load_next(v[1]);
+                };
+                if constexpr (LOADS == SCALES_PAIR) {
+                    if ((kb & 1) == 0) advance();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        c[i] = (kb & 1) == 0 ? make_uint2(v[0][i][0], v[0][i][1]) : make_uint2(v[0][i][2], v[0][i][3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (LOADS == SCALES_WIDE) {
+                            c[i] = make_uint2(v[0][i][0], v[0][i][1]);
+                        } else {
+                            const int r = half * 128 + lane + 32 * i;
+                            c[i] = scale_bytes(v[0][i], scales, static_cast<int64_t>(r0 + r) * p.G + (kb0 + kb) * 8, table,
+                                               r < span && r0 + r < rows, p.G - (kb0 + kb) * 8);
+                        }
+                    }
+                    advance();
                 }
                 if (it >= kStages) ok = mbar_wait(empty(s), ((it / kStages) - 1) & 1, p.status);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -442,11 +467,11 @@ void pick_plan(int64_t m, int64_t N, int num_kb, int sms, int* bn_out, int* s_ou
     }
 }
 
-template <bool WIDE>
+template <ScaleLoads LOADS>
 cudaError_t launch(unsigned grid, const CUtensorMap& tm_w, const CUtensorMap& tm_a, const MatmulParams& p, cudaStream_t stream) {
     static std::atomic<int> configured[64];
     const size_t smem = kStages * kStageBytes + 1024;
-    cudaError_t e = ensure_dynamic_smem(k_mx4_matmul<WIDE>, smem, configured);
+    cudaError_t e = ensure_dynamic_smem(k_mx4_matmul<LOADS>, smem, configured);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
@@ -462,7 +487,7 @@ cudaError_t launch(unsigned grid, const CUtensorMap& tm_w, const CUtensorMap& tm
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.S > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, k_mx4_matmul<WIDE>, tm_w, tm_a, p);
+    return cudaLaunchKernelEx(&cfg, k_mx4_matmul<LOADS>, tm_w, tm_a, p);
 }
 
 }  // namespace
@@ -479,8 +504,12 @@ cudaError_t launch_mx4_matmul(const Mx4View& w, const Mx4View& a, void* y, cudaS
     p.G = static_cast<int>(w.cols / kMxBlock);
     p.num_kb = static_cast<int>((w.cols + kBK - 1) / kBK);
     pick_plan(a.rows, w.rows, p.num_kb, sms, &p.BN, &p.S);
-    const bool a8 = ((reinterpret_cast<uintptr_t>(w.scales) | reinterpret_cast<uintptr_t>(a.scales)) & 7u) == 0;
-    const bool wide = p.G % 8 == 0 && a8;
+    const uintptr_t tables = reinterpret_cast<uintptr_t>(w.scales) | reinterpret_cast<uintptr_t>(a.scales);
+    const bool wide = p.G % 8 == 0 && (tables & 7u) == 0;
+    // Pairs halve the sectors fetched, which counts where many tiles run (8192 x 14336 x
+    // 4096: 238 -> 222 us, 8192 x 4096 x 14336: 205 -> 200); with K split, latency
+    // counts, and they measured slower (64 x 4096 x 14336: 16.2 -> 16.6 us).
+    const bool pair = p.S == 1 && p.G % 16 == 0 && (tables & 15u) == 0;
     // kind::mxf4: A and B E2M1 (1), scales UE8M0 (bit 23), N / 8, M / 128
     p.idesc = 1u << 7 | 1u << 10 | static_cast<uint32_t>(p.BN / 8) << 17 | 1u << 23 | 1u << 27;
     p.status = device_status_ptr();
@@ -493,7 +522,8 @@ cudaError_t launch_mx4_matmul(const Mx4View& w, const Mx4View& a, void* y, cudaS
     const int64_t tiles = ((w.rows + kBM - 1) / kBM) * ((a.rows + p.BN - 1) / p.BN);
     if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;
     const unsigned grid = static_cast<unsigned>(p.S > 1 ? tiles * p.S : (tiles < sms ? tiles : sms));
-    return wide ? launch<true>(grid, tm_w, tm_a, p, stream) : launch<false>(grid, tm_w, tm_a, p, stream);
+    return pair ? launch<SCALES_PAIR>(grid, tm_w, tm_a, p, stream)
+                : (wide ? launch<SCALES_WIDE>(grid, tm_w, tm_a, p, stream) : launch<SCALES_ANY>(grid, tm_w, tm_a, p, stream));
 }
 
 }  // namespace mlxq
