@@ -318,9 +318,9 @@ __global__ void __launch_bounds__(AsyncSmem<NT>::kThreads, 1) k_mx4_gemm_async(c
                 // all groups have read it: one warp of each kw sees to it, the groups
                 // taking turns.
                 const int next = it + stages - wk;
-                if (it >= wk && next < total && ((next >> lw) & (groups - 1)) == group && ok) {
+                if (it >= wk && next < total && ((next >> lw) & (groups - 1)) == group) {
                     const int s = stage >= wk ? stage - wk : stage - wk + stages;
-                    ok = mbar_wait(empty(s), stage >= wk ? parity : parity ^ 1u, p.status);
+                    if (ok) ok = mbar_wait(empty(s), stage >= wk ? parity : parity ^ 1u, p.status);
                     if (lane == 0 && ok) feed_x(s, k + ahead < padded ? k + ahead : k + ahead - padded);
                     __syncwarp();
                 }
