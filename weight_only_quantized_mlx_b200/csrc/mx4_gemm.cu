@@ -16,7 +16,7 @@
 // which the products take it, step after step, and bulk copies bring the steps into
 // a ring while the warps multiply.  Where rows are few, four blocks of a cluster share
 // a range of rows and split K, which divides the copies of X, and add their sums
-// through distributed shared memory in rank order.  28672 x 8192: 16 rows 67 us, 32
+// through distributed shared memory in rank order.  28672 x 8192: 16 rows 65 us, 32
 // rows 92, 64 rows 171; 4096 x 4096: 14, 16, 19.  The products bound it (without
 // them 33 us whatever the rows at 28672 x 8192; without the copies of the weight 64,
 // 93 and 145).
