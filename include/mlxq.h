@@ -293,8 +293,9 @@ MLXQ_API int mlxq_mx4_matmul(const mlxq_mx4* w, const mlxq_mx4* a, void* y, uint
  * aligned).  The experts' weights are stacked: gate and up have experts * inter
  * rows of hidden columns, down experts * hidden rows of inter columns; rows of
  * expert e follow those of expert e - 1.  1 <= experts <= 256, 1 <= top_k <=
- * min(experts, 16).  The gated product is rounded once, to BF16, before the down
- * projection; all sums are fp32.
+ * min(experts, 16).  The gated product p silu(..) * (..) is held to 2^-16 of itself
+ * before the down projection (MX4, m > 4: to 2^-11, and to 2^-39 of its token's and
+ * expert's largest); all sums are fp32, and y is rounded once.
  *   mlxq_moe      8-bit weights; hidden and inter multiples of 64, group_size 32,
  *                 64 or 128 (one for gate and up), codes 16-byte and tables
  *                 4-byte aligned.  Weight flags are ignored.

@@ -1,0 +1,79 @@
+"""GPU numerics of the expert layer beyond its parity tests: how h = p silu(g) u is
+held between the projections, sums over the experts, ties and ends of the ranges."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import _mx4_ref as ref
+import synth
+import weight_only_quantized_mlx_b200 as mq
+from _helpers import dev
+from test_gpu_moe import Layer, f64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    mq.lib()
+    yield
+    torch.cuda.synchronize()
+    mq.mlxq_device_status()
+
+
+def layer_of_integers(seed, E, H, I, group):
+    """Experts whose gate and up sums over small integers are exact in fp32 in any order."""
+    L = Layer(seed, E, H, I, group)
+    L.handles, L.values, L.keep = [], [], []
+    for rows, cols in ((E * I, H), (E * I, H), (E * H, I)):
+        if group:  # (q - 128) 2^-k
+            k = 2.0 ** -round(math.log2(74 * math.sqrt(cols)))
+            q = L.g.integers(0, 256, (rows, cols)).astype(np.uint32)
+            p = (q.reshape(rows, -1, 4) << (8 * np.arange(4, dtype=np.uint32))).sum(axis=-1, dtype=np.uint32)
+            s = np.full((rows, cols // group), k)
+            L.keep.append((dev(p), dev(synth.to_bf16_bits(s)), dev(synth.to_bf16_bits(-128.0 * s))))
+            L.handles.append(mq.weight_view(*L.keep[-1], group))
+            v = (q.astype(np.float64) - 128.0) * k
+        else:
+            e = 127 + round(math.log2(1 / (2.9 * math.sqrt(cols))))
+            codes, scales = ref.random_weight(L.g, rows, cols, low=e, high=e + 1)
+            L.handles.append(mq.mx4_view(dev(ref.pack(codes)), dev(scales)))
+            v = ref.values(codes, scales)
+        L.values.append(torch.from_numpy(v).cuda().reshape(E, -1, cols))
+    return L
+
+
+@pytest.mark.parametrize("group", [64, 0], ids=["gs64", "mx4"])
+@pytest.mark.parametrize("m,k", [(1, 1), (4, 1), (5, 2), (8, 1), (12, 1), (64, 1), (64, 2)])
+def test_h_is_held_to_eleven_bits(m, k, group):
+    """Gate and up are exact here, so what is off beside y's own rounding is how h is held."""
+    E, H, I = 4, 64, 64
+    L = layer_of_integers(50 + m, E, H, I, group)
+    xb = synth.to_bf16_bits(L.g.integers(-4, 5, (m, H)).astype(np.float64))
+    y = L.run(dev(xb), k).double()
+    x = f64(xb)
+    gate, up, down = L.values
+    logits = x @ f64(L.router_bits).t()
+    ids = torch.sort(logits, dim=1, descending=True, stable=True)[1][:, :k]
+    want, slack = torch.zeros_like(x), torch.zeros_like(x)
+    # fp32 sums on the tensor pipe: each of the MMAs (16 products, h in up to two parts) loses at most 2^-22 of the magnitudes
+    gi = (2 * k * I / 16 + 32) * 2.0 ** -22
+    for t in range(m):
+        w = torch.exp(logits[t] - logits[t].max())
+        for e in ids[t].tolist():
+            g, u = gate[e] @ x[t], up[e] @ x[t]
+            h = w[e] / w[ids[t]].sum() * g / (1 + torch.exp(-g)) * u
+            # 2^-11: h as FP16 (as two BF16 parts 2^-16); 2^-39 of the largest: below FP16's normal numbers;
+            # 2^-18: expf, the division, p and the products
+            dh = (2.0 ** -11 + 2.0 ** -18) * h.abs() + 2.0 ** -39 * h.abs().max()
+            want[t] += down[e] @ h
+            slack[t] += down[e].abs() @ (dh + gi * h.abs())
+    off = (y - want).abs()
+    assert (off <= slack + 2.0 ** -8 * (want.abs() + slack)).all()
+    # y's rounding: at most 2^-8, 2^-8 / sqrt(3) in the mean; h's the same with 2^-11
+    assert float(off.norm() / want.norm()) <= math.hypot(2.0 ** -8, 2.0 ** -11) / math.sqrt(3)

@@ -23,8 +23,15 @@
 // 25 us (4), a chain of latencies: router 5 us, lists 1.4, first copies and
 // activations 2.3, gate and up 5, barrier 3.5, down 4.2.
 //
-// Rounding: h is rounded to BF16 once (with p in it), the operand type of the
-// tensor pipe; sums, silu and p are fp32.
+// Rounding: the tensor pipe takes 16-bit operands, and one BF16 value for h (with p in
+// it) showed in y (relative error 2.4e-3 against 1.7e-3 of y's own rounding).  So h is
+// held as the sum of two BF16 values, a column of the down product each, to 2^-16 of
+// itself; or, for MX4 and more than four tokens, as FP16 in units of the slot's
+// largest power of two, to 2^-11 (and to 2^-39 of the largest), for which the blocks
+// write fp32, cross a barrier and convert a share each: half the products, and the
+// codes need no BF16 form (64 tokens, 128 experts of 4128 x 1504: 480 us against 535 with
+// two parts; 8 tokens, 64 experts of 2048 x 1024: 63 against 72; 64 tokens, 8 of 32 experts: 128
+// against 142).  With BF16 weights FP16 is not open.  Sums, silu and p are fp32.
 #include <cooperative_groups.h>
 
 #include <utility>
@@ -41,23 +48,34 @@ constexpr int kRouterCluster = 8;
 constexpr int kRouterWarps = 16;
 
 // Workspace (see moe_workspace_bytes): 256 bytes holding the barrier count,
-// ids [slots], shares [slots], h [slots][inter].
+// ids [slots], shares [slots], largest exponents [slots], h.  Where h is the sum of two
+// BF16 parts: h [slots][F::h_row(inter)], in the order in which the down phase reads it
+// (F::place); else raw [slots][inter] fp32 and h [slots][inter] FP16, made of raw.
+constexpr int kHStep = 128;  // F::h_row is at most 2 inter rounded up to it
 struct MoeWorkspace {
     unsigned int* barrier;
     int* ids;
     float* share;
+    uint32_t* top;
+    float* raw;
     uint16_t* h;
 };
 
 int64_t align256(int64_t v) { return (v + 255) & ~int64_t{255}; }
 
-MoeWorkspace carve(void* ws, int64_t slots) {
+int64_t raw_bytes(int64_t inter, int64_t slots) { return align256(slots * ((inter + kHStep - 1) / kHStep * kHStep) * 4); }
+
+MoeWorkspace carve(void* ws, int64_t inter, int64_t slots, bool pair) {
     uint8_t* b = static_cast<uint8_t*>(ws);
+    const int64_t per_slot = align256(slots * 4);
     MoeWorkspace r;
     r.barrier = reinterpret_cast<unsigned int*>(b);
     r.ids = reinterpret_cast<int*>(b + 256);
-    r.share = reinterpret_cast<float*>(b + 256 + align256(slots * 4));
-    r.h = reinterpret_cast<uint16_t*>(b + 256 + 2 * align256(slots * 4));
+    r.share = reinterpret_cast<float*>(b + 256 + per_slot);
+    r.top = reinterpret_cast<uint32_t*>(b + 256 + 2 * per_slot);
+    b += 256 + 3 * per_slot;
+    r.raw = reinterpret_cast<float*>(b);
+    r.h = reinterpret_cast<uint16_t*>(pair ? b : b + raw_bytes(inter, slots));
     return r;
 }
 
@@ -171,6 +189,7 @@ __global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(kRouter
         const int s = (t0 + warp) * p.top_k + lane;
         p.ws.ids[s] = mine_e;
         p.ws.share[s] = __fdiv_rn(expf(mine_v - first), sum);
+        p.ws.top[s] = 0u;
     }
 }
 
@@ -202,8 +221,10 @@ struct ExpertLists {
     int16_t off[kMaxEntries];    // its first column
     int16_t cnt[kMaxEntries];    // its columns
     int16_t cols[kMaxListed];    // slots
+    uint8_t field[kMaxListed];   // their largest exponent fields, where h is FP16
     long long before[kMaxEntries + 1];  // NT > 1: weight of all gate and up rows before entry a's
     int entries;
+    int columns;                 // places of `cols` in use
     int stop;
 
     // What a row of entry a costs: some fixed work, and the products of its column
@@ -258,7 +279,10 @@ __device__ __forceinline__ void build_lists(ExpertLists& L, const int* ids, int 
             a += total & 0xFFFF;
             o += total >> 16;
         }
-        if (lane == 0) L.entries = a;
+        if (lane == 0) {
+            L.entries = a;
+            L.columns = o;
+        }
     }
     __syncthreads();
     for (int s = tid; s < slots; s += kStreamThreads) {
@@ -292,9 +316,9 @@ __device__ __forceinline__ void build_lists(ExpertLists& L, const int* ids, int 
     __syncthreads();
 }
 
-// Every block has passed its writes of h.  Bounded: false (and a status bit)
-// when the others do not arrive.
-__device__ __forceinline__ bool grid_barrier(unsigned int* count, unsigned int* status, int* stop) {
+// Every block has come here `times` times, its writes before are seen.  Bounded:
+// false (and a status bit) when the others do not arrive.
+__device__ __forceinline__ bool grid_barrier(unsigned int* count, unsigned int times, unsigned int* status, int* stop) {
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
@@ -304,7 +328,7 @@ __device__ __forceinline__ bool grid_barrier(unsigned int* count, unsigned int* 
         for (uint32_t it = 1;; ++it) {
             unsigned int v;
             asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
-            if (v >= gridDim.x) break;
+            if (v >= times * gridDim.x) break;
             if ((it & 63u) == 0u && globaltimer_ns() - t0 > kWaitLimitNs) {
                 atomicOr(status, MLXQ_STATUS_TIMEOUT);
                 gave_up = 1;
@@ -335,12 +359,23 @@ struct Smem {
     static_assert(kAreas + kStreamWarps * kDownArea <= kTotal && kDownArea % 16 == 0, "areas of the down phase");
 };
 
+// h as two parts that BF16 takes: its top half, cut (so that it is finite where h is), and the
+// rest, which the caller rounds (to 2^-9 of 2^-7 of h).  Neither is zero where h is
+// not, since an infinite weight times zero would be NaN: an h that BF16 holds whole
+// comes as two halves, and so do infinities and NaN.  (Next to BF16's subnormals a half
+// would lose a bit: there the rest is zero.)
+__device__ __forceinline__ float2 two_parts(float h) {
+    const float top = __uint_as_float(__float_as_uint(h) & 0xFFFF0000u), rest = h - top;
+    if (fabsf(rest) > 0.f || fabsf(h) < 0x1p-100f) return make_float2(top, rest);
+    return make_float2(0.5f * h, 0.5f * h);
+}
+
 // gate and up, then h = p silu(gate) up, for the flattened rows [lo, hi) of
 // (hit experts) x I, in octets (I % 8 == 0): a tile is 8 gate rows and the
 // same 8 up rows, so the lane that holds a gate sum holds its up sum.  With up
 // to 8 tokens all tiles are one segment (column = token), else a segment is an
 // expert (columns = its tokens).
-template <class F, int NT>
+template <class F, class FD, int NT>
 struct GateUpJob {
     const ExpertParams<F>& p;
     const typename F::Mat& mat;
@@ -392,33 +427,76 @@ struct GateUpJob {
         return F::row_key(p.gate, static_cast<uint32_t>(L.act[a]) * static_cast<uint32_t>(p.I) +
                                       static_cast<uint32_t>((o - a * per) * 8 + (lane >> 2)));
     }
+    // (all lanes of a warp, for one tile)
     __device__ __forceinline__ void store(int s, int tile, int n, int lane, const float4& v) const {
         const int o = o0 + tile, a = o / per, g = lane >> 2;
         const int64_t flat = 8 * static_cast<int64_t>(o) + g;
-        if (flat < lo || flat >= hi) return;
+        const bool live = flat >= lo && flat < hi;
         const int row = (o - a * per) * 8 + g;
         const float gate[2] = {v.x, v.y}, up[2] = {v.z, v.w};
+        uint32_t field = 0;  // both columns' exponent fields, 16 bits each
+        int slot[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int c = n * 8 + 2 * (lane & 3) + i;
-            const int slot = c < cols(s) ? cm.slot(a, c) : -1;
-            if (slot < 0) continue;
-            const float h = p.ws.share[slot] * (__fdiv_rn(gate[i], 1.0f + expf(-gate[i])) * up[i]);
-            p.ws.h[static_cast<int64_t>(slot) * p.I + F::place(row)] = static_cast<uint16_t>(pack_bf16x2(h, 0.f));
+            slot[i] = c < cols(s) ? cm.slot(a, c) : -1;
+            if (slot[i] < 0 || !live) continue;
+            const float h = p.ws.share[slot[i]] * (__fdiv_rn(gate[i], 1.0f + expf(-gate[i])) * up[i]);
+            if constexpr (FD::kPair) {
+                uint16_t* at = p.ws.h + static_cast<int64_t>(slot[i]) * FD::h_row(p.I) + FD::place(row);
+                const float2 parts = two_parts(h);
+                at[0] = static_cast<uint16_t>(__float_as_uint(parts.x) >> 16);
+                at[32] = static_cast<uint16_t>(pack_bf16x2(parts.y, 0.f));
+            } else {
+                p.ws.raw[static_cast<int64_t>(slot[i]) * p.I + row] = h;
+                field |= (__float_as_uint(h) >> 23 & 255u) << (16 * i);
+            }
+        }
+        if constexpr (!FD::kPair) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) field = __vmaxu2(field, __shfl_xor_sync(0xFFFFFFFFu, field, d));
+            if (g == 0) {  // the same columns' eight rows: one lane tells
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (slot[i] >= 0) atomicMax(p.ws.top + slot[i], field >> (16 * i) & 0xFFFFu);
+            }
         }
     }
 };
 
+// raw -> h, the grid's blocks a share each; and the list's exponent fields.
+template <class Params>
+__device__ __forceinline__ void convert_h(const Params& p, ExpertLists& L, int listed) {
+    const int per = p.I >> 3, pieces = p.m * p.top_k * per;  // (1024 slots of 2^17 pieces at most)
+    for (int i = blockIdx.x * kStreamThreads + threadIdx.x; i < pieces; i += gridDim.x * kStreamThreads) {
+        const float f = x_inverse(p.ws.top[i / per]);
+        const float4* from = reinterpret_cast<const float4*>(p.ws.raw) + 2 * static_cast<int64_t>(i);
+        const float4 a = from[0], b = from[1];
+        uint4 v;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v.x) : "f"(a.y * f), "f"(a.x * f));
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v.y) : "f"(a.w * f), "f"(a.z * f));
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v.z) : "f"(b.y * f), "f"(b.x * f));
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v.w) : "f"(b.w * f), "f"(b.z * f));
+        reinterpret_cast<uint4*>(p.ws.h)[i] = v;
+    }
+    for (int c = threadIdx.x; c < listed; c += kStreamThreads) {
+        const int s = L.cols[c];
+        L.field[c] = static_cast<uint8_t>(s >= 0 ? p.ws.top[s] : 0u);
+    }
+}
+
 // y[token][row] = sum over hit experts a and columns k of Wd_a[row, k] h[slot][k]
 // for the block's rows [lo, hi).  Tiles are 16 rows; every expert's slice of a
 // tile goes into one accumulator, so the sum over experts needs no second pass
-// and no atomics: with up to 8 tokens column = token and each expert's fragment
-// is added, where the token chose the expert, else each warp adds an expert's columns to its own
-// [16][tokens] sums in shared memory.  The warps that share a tile join in warp
-// order, so results do not depend on timing.  h is read once or twice per
-// block, so it is not staged: a lane loads the next step's first column tile
-// before it multiplies the present one.  `ready` runs once the ring has been
-// filled (weights only) and before h is read; false ends the phase.
+// and no atomics: with up to 8 tokens column = token and each expert's fragment is
+// added, where the token chose the expert, else each warp adds an expert's columns to
+// its own [16][tokens] sums in shared memory.  The warps that share a tile join in
+// warp order, so results do not depend on timing.  Where h has two parts (F::kPair)
+// a column tile holds four slots, both parts of each side by side, so that one lane
+// gets both parts' sums; else eight.  h is read once or twice per block, so it is not
+// staged: a lane loads the next step's first column tile before it multiplies the
+// present one.  `ready` runs once the ring has been filled (weights only) and before h
+// is read; false ends the phase.
 template <class F, int NT, class Params, class Ready>
 __device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L, const Columns& cm, uint32_t ring,
                                            uint8_t* areas, Ready ready) {
@@ -452,6 +530,11 @@ __device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L
     constexpr int kBatch = NT == 1 ? 4 : 1;           // tiles between two joins
     constexpr int kAreaFloats = Smem<NT>::kDownArea / 4;
     constexpr int kStride = Smem<NT>::kTokens + 1;    // NT > 1: floats per row of the area
+    constexpr int kSlots = F::kPair ? 4 : 8;          // slots of a column tile
+    constexpr int DT = 8 * NT / kSlots;               // column tiles of an entry
+    // The first tile's h is loaded a step ahead, except with four tiles of MX4, whose registers
+    // do not reach (64 tokens, 8 of 32 experts of 2048 x 1024: 132 us with it, 128 without).
+    constexpr bool kAhead = F::kPieces == 2 || NT < 4;
     float* area = reinterpret_cast<float*>(areas + warp * Smem<NT>::kDownArea);
     const float* group_area = reinterpret_cast<const float*>(areas + group * wk * Smem<NT>::kDownArea);
 
@@ -493,13 +576,13 @@ __device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L
         for (; batch < kBatch; ++batch) {
             const int tile = tile0 + batch * groups;
             if (tile >= tiles) break;
-            float acc[NT][4];
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};  // NT == 1: over the experts
-            const uint16_t* xp[NT];  // this lane's rows of h, at its place in a step
+            float acc[DT][4];
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};  // NT == 1: over the experts; rows g and g + 8 of one slot, then of another
+            int xp[DT];  // this lane's rows of h, at its place in a step, in units of 8 values; -1: none
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+            for (int n = 0; n < DT; ++n) {
                 acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-                xp[n] = nullptr;
+                xp[n] = -1;
             }
             if (NT > 1) {
                 for (int i = lane; i < 16 * kStride; i += 32) area[i] = 0.f;
@@ -507,76 +590,103 @@ __device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L
             }
             auto scatter = [&](int a, int nt) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int n = 0; n < DT; ++n) {
                     if (n >= nt) break;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int s = cm.slot(a, n * 8 + 2 * t + i);
+                    if constexpr (F::kPair) {
+                        const int s = cm.slot(a, n * 4 + t);
                         if (s >= 0) {
                             const int token = s / cm.top_k;
-                            area[g * kStride + token] += acc[n][i];
-                            area[(g + 8) * kStride + token] += acc[n][2 + i];
+                            area[g * kStride + token] += acc[n][0] + acc[n][1];
+                            area[(g + 8) * kStride + token] += acc[n][2] + acc[n][3];
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int s = cm.slot(a, n * 8 + 2 * t + i);
+                            if (s >= 0) {
+                                const int token = s / cm.top_k;
+                                area[g * kStride + token] += acc[n][i];
+                                area[(g + 8) * kStride + token] += acc[n][2 + i];
+                            }
                         }
                     }
                     acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
                 }
                 __syncwarp();
             };
-            auto column = [&](int a, int n) -> const uint16_t* {
-                const int s = cm.slot(a, n * 8 + g);
-                return s >= 0 ? p.ws.h + static_cast<int64_t>(s) * p.I + t * (8 * F::kPieces) : nullptr;
+            auto column = [&](int a, int n) {
+                const int s = cm.slot(a, F::kPair ? n * 4 + (g >> 1) : n * 8 + g);
+                if (s < 0) return -1;
+                if constexpr (F::kPair) return s * (F::h_row(p.I) >> 3) + (g & 1) * 4 + t;  // (< 2^28)
+                else return s * (p.I >> 3) + t;
             };
-            // pieces of the lane's row of h for a step; zeros where there is none
-            auto fetch = [&](uint4 (&v)[F::kPieces], const uint16_t* row, int step) {
-                const int k = step * F::kStepCols;
-                const bool in = row != nullptr && k + t * (8 * F::kPieces) < p.I;
+            // piece i of the lane's row of h for a step; zeros where there is none
+            auto piece = [&](int row, int step, int i) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                const bool in = F::kPair ? step * F::kStepCols + t * (8 * F::kPieces) < p.I : step * F::kStepCols + 32 * i < p.I;
+                if (row >= 0 && in)
+                    v = ldg128(reinterpret_cast<const uint4*>(p.ws.h) + row +
+                               (F::kPair ? (step * F::kPieces + i) * 8 : step * (F::kStepCols / 8) + 4 * i));
+                return v;
+            };
+            auto fetch = [&](uint4 (&v)[F::kPieces], int row, int step) {
 #pragma unroll
-                for (int i = 0; i < F::kPieces; ++i) {
-                    v[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (in) v[i] = ldg128(row + k + 8 * i);
-                }
+                for (int i = 0; i < F::kPieces; ++i) v[i] = piece(row, step, i);
             };
             uint4 x0[F::kPieces];
-            const uint16_t* row0 = nullptr;  // h of column tile 0
+            int row0 = -1;  // h of column tile 0
             if (!idle) {
                 row0 = column(a0, 0);
-                fetch(x0, row0, s0);
+                if (kAhead) fetch(x0, row0, s0);
             }
             for (int a = a0; a < a1 && !idle; ++a) {
-                const int nt = NT == 1 ? 1 : (cm.cnt[a] + 7) / 8;
+                const int nt = ((NT == 1 ? p.m : cm.cnt[a]) + kSlots - 1) / kSlots;
 #pragma unroll
-                for (int n = 1; n < NT; ++n) xp[n] = n < nt ? column(a, n) : nullptr;
+                for (int n = 1; n < DT; ++n) xp[n] = n < nt ? column(a, n) : -1;
                 const uint32_t key = F::row_key(p.down, static_cast<uint32_t>(L.act[a]) * static_cast<uint32_t>(p.H) +
                                                             static_cast<uint32_t>(lo + tile * 16 + g));
-                const uint16_t* next0 = a + 1 < a1 ? column(a + 1, 0) : nullptr;
+                const int next0 = a + 1 < a1 ? column(a + 1, 0) : -1;
+                [[maybe_unused]] bool plain = true;  // sums are in the columns' units (FP16)
+                [[maybe_unused]] auto unit = [&](int c) { return x_unit(L.field[cm.off[a] + min(c, nt * 8 - 1)]); };
                 // N column tiles, a power of two: unused ones are zeros
                 auto run = [&](auto count) {
-                    constexpr int N = decltype(count)::value < NT ? decltype(count)::value : NT;
+                    constexpr int N = decltype(count)::value < DT ? decltype(count)::value : DT;
 #pragma unroll 1
                     for (int step = s0; step < S; step += turns) {
                         const bool turn = step + turns >= S;
                         uint4 x1[F::kPieces];
-                        fetch(x1, turn ? next0 : row0, turn ? s0 : step + turns);
+                        if (kAhead) fetch(x1, turn ? next0 : row0, turn ? s0 : step + turns);
                         cp_async_wait<kDepth - 2>();
                         __syncwarp();  // the copies of all lanes have landed; the slot refilled below is read out
                         issue();
-                        const int k = step * F::kStepCols;
-                        const bool in = k + t * (8 * F::kPieces) < p.I;
-                        F::template consume<NT, N>(p.down, cslot, lane, key, step, acc, [&](int i, int n) {
-                            if (n == 0) return x0[i];
-                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                            if (xp[n] != nullptr && in) v = ldg128(xp[n] + k + 8 * i);
+                        auto x = [&](int i, int n) {
+                            if (n > 0 || !kAhead) return piece(n > 0 ? xp[n] : row0, step, i);
+                            uint4 v = x0[0];  // (not indexed: a loop over i may stay one, and x0 has to stay in registers)
+#pragma unroll
+                            for (int j = 1; j < F::kPieces; ++j)
+                                if (i == j) v = x0[j];
                             return v;
-                        });
+                        };
+                        if constexpr (F::kPair) {
+                            F::template consume<DT, N>(p.down, cslot, lane, key, step, acc, x);
+                        } else {
+                            const uint32_t keys[1] = {key};
+                            F::template consume_tiles<1, DT, N>(p.down, cslot, lane, keys, step, reinterpret_cast<float(&)[1][DT][4]>(acc), plain,
+                                                                x, unit);
+                        }
                         cslot = cslot == ring + kRingBytes - kStageBytes ? ring : cslot + kStageBytes;
 #pragma unroll
-                        for (int i = 0; i < F::kPieces; ++i) x0[i] = x1[i];
+                        for (int i = 0; i < F::kPieces && kAhead; ++i) x0[i] = x1[i];
                     }
                 };
-                if (NT == 1 || nt == 1) run(std::integral_constant<int, 1>{});
-                else if (NT == 2 || nt == 2) run(std::integral_constant<int, 2>{});
-                else run(std::integral_constant<int, 4>{});
+                if (DT == 1 || nt == 1) run(std::integral_constant<int, 1>{});
+                else if (DT == 2 || nt == 2) run(std::integral_constant<int, 2>{});
+                else if (DT == 4 || nt <= 4) run(std::integral_constant<int, 4>{});
+                else run(std::integral_constant<int, 8>{});
                 row0 = next0;
+                if constexpr (!F::kPair) {
+                    if (plain) F::template to_numbers<DT>(acc, t, unit);
+                }
                 if (NT > 1) {
                     scatter(a, nt);
                 } else {
@@ -584,12 +694,13 @@ __device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L
                     // times an infinite or NaN weight would not be zero
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        if (cm.slot(a, 2 * t + i) >= 0) {
-                            sum[i] += acc[0][i];
-                            sum[2 + i] += acc[0][2 + i];
-                        }
-                        acc[0][i] = acc[0][2 + i] = 0.f;
+                        const int n = F::kPair ? i : 0;
+                        if (cm.slot(a, F::kPair ? 4 * i + t : 2 * t + i) < 0) continue;
+                        sum[2 * i] += F::kPair ? acc[n][0] + acc[n][1] : acc[n][i];
+                        sum[2 * i + 1] += F::kPair ? acc[n][2] + acc[n][3] : acc[n][2 + i];
                     }
+#pragma unroll
+                    for (int n = 0; n < DT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
                 }
             }
             if (NT == 1) reinterpret_cast<float4*>(area)[batch * 32 + lane] = make_float4(sum[0], sum[1], sum[2], sum[3]);
@@ -606,13 +717,16 @@ __device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L
                     s.z += q.z;
                     s.w += q.w;
                 }
-                const int r = lo + (tile0 + (i >> 5) * groups) * 16 + ((i & 31) >> 2), c = 2 * (i & 3);
+                const int r = lo + (tile0 + (i >> 5) * groups) * 16 + ((i & 31) >> 2), q = i & 3;
                 const uint32_t b0 = pack_bf16x2(s.x, s.y), b1 = pack_bf16x2(s.z, s.w);
-                uint16_t* y = p.y + static_cast<int64_t>(c) * p.H + r;
-                if (c < p.m && r < hi) y[0] = static_cast<uint16_t>(b0);
-                if (c + 1 < p.m && r < hi) y[p.H] = static_cast<uint16_t>(b0 >> 16);
-                if (c < p.m && r + 8 < hi) y[8] = static_cast<uint16_t>(b1);
-                if (c + 1 < p.m && r + 8 < hi) y[p.H + 8] = static_cast<uint16_t>(b1 >> 16);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int c = F::kPair ? 4 * j + q : 2 * q + j;
+                    uint16_t* y = p.y + static_cast<int64_t>(c) * p.H + r;
+                    const uint32_t b = j == 0 ? b0 : b1;
+                    if (c < p.m && r < hi) y[0] = static_cast<uint16_t>(b);
+                    if (c < p.m && r + 8 < hi) y[8] = static_cast<uint16_t>(b >> 16);
+                }
             }
         } else {
             const int r0 = lo + tile0 * 16;
@@ -641,9 +755,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_moe_experts(const __grid_
     build_lists<NT>(L, p.ws.ids, p.m * p.top_k, p.top_k, p.E, p.I);
     const Columns cm{L.cols, L.off, L.cnt, p.top_k};
     const XBuffer xb{smem_u32(smem) + M::kX, static_cast<int>(M::kXBytes), field, field + kMoeMaxTokens};
-    shared_phase<FG, NT>(GateUpJob<FG, NT>(p, L, cm), ring, smem + M::kAreas, xb);
+    shared_phase<FG, NT>(GateUpJob<FG, FD, NT>(p, L, cm), ring, smem + M::kAreas, xb);
     __syncthreads();  // the groups of the next phase are others, and its areas lie over the activations
-    down_phase<FD, NT>(p, L, cm, ring, smem + M::kAreas, [&] { return grid_barrier(p.ws.barrier, p.status, &L.stop); });
+    down_phase<FD, NT>(p, L, cm, ring, smem + M::kAreas, [&] {
+        if (!grid_barrier(p.ws.barrier, 1u, p.status, &L.stop)) return false;
+        if constexpr (FD::kPair) return true;
+        convert_h(p, L, L.columns);
+        return grid_barrier(p.ws.barrier, 2u, p.status, &L.stop);
+    });
 }
 
 template <int TB>
@@ -672,9 +791,9 @@ cudaError_t launch_experts(const ExpertParams<FG>& p, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, k_moe_experts<FG, FD, NT>, p);
 }
 
-template <class FG, class FD, class View>
-cudaError_t launch_moe_any(const MoeCall& c, const View& gate, const View& up, const View& down, cudaStream_t stream) {
-    const MoeWorkspace ws = carve(c.workspace, static_cast<int64_t>(c.m) * c.top_k);
+template <class FG, class FD, int NT, class View>
+cudaError_t launch_both(const MoeCall& c, const View& gate, const View& up, const View& down, cudaStream_t stream) {
+    const MoeWorkspace ws = carve(c.workspace, c.inter, static_cast<int64_t>(c.m) * c.top_k, FD::kPair);
     const RouterParams r{static_cast<const uint16_t*>(c.router), static_cast<const uint16_t*>(c.x), c.experts, c.hidden, c.m,
                          c.top_k, c.softmax_all, ws};
     // few tokens: a cluster each; more: several tokens share a pass over the
@@ -683,17 +802,22 @@ cudaError_t launch_moe_any(const MoeCall& c, const View& gate, const View& up, c
     if (e != cudaSuccess) return e;
     const ExpertParams<FG> p{FG::make(gate), FG::make(up), FD::make(down), static_cast<const uint16_t*>(c.x),
                             static_cast<uint16_t*>(c.y), c.experts, c.hidden, c.inter, c.m, c.top_k, ws, device_status_ptr()};
-    if (c.m <= 8) return launch_experts<FG, FD, 1>(p, stream);
+    return launch_experts<FG, FD, NT>(p, stream);
+}
+
+template <class FG, class FD, class View>
+cudaError_t launch_moe_any(const MoeCall& c, const View& gate, const View& up, const View& down, cudaStream_t stream) {
+    if (c.m <= 8) return launch_both<FG, FD, 1>(c, gate, up, down, stream);
     // Two column tiles where experts have up to 8 tokens on average: fewer registers,
     // and the few experts with more than 16 are streamed again.
-    if (c.m <= 16 || c.m * c.top_k <= 8 * c.experts) return launch_experts<FG, FD, 2>(p, stream);
-    return launch_experts<FG, FD, 4>(p, stream);
+    if (c.m <= 16 || c.m * c.top_k <= 8 * c.experts) return launch_both<FG, FD, 2>(c, gate, up, down, stream);
+    return launch_both<FG, FD, 4>(c, gate, up, down, stream);
 }
 
 }  // namespace
 
 size_t moe_workspace_bytes(int64_t inter, int64_t slots) {
-    return static_cast<size_t>(256 + 2 * align256(slots * 4) + align256(slots * inter * 2));
+    return static_cast<size_t>(256 + 3 * align256(slots * 4) + raw_bytes(inter, slots) + align256(slots * inter * 2));
 }
 
 cudaError_t launch_moe(const MoeCall& c, const WeightView& gate, const WeightView& up, const WeightView& down,
@@ -703,7 +827,10 @@ cudaError_t launch_moe(const MoeCall& c, const WeightView& gate, const WeightVie
 
 cudaError_t launch_mx4_moe(const MoeCall& c, const Mx4View& gate, const Mx4View& up, const Mx4View& down,
                            cudaStream_t stream) {
-    return launch_moe_any<Mx4HalfFmt, Mx4Fmt>(c, gate, up, down, stream);
+    // Up to four tokens fit a column tile with both parts of h, which needs no second
+    // barrier and no pass over h in between (about 3 us).
+    if (c.m <= 4) return launch_both<Mx4HalfFmt, Mx4Fmt, 1>(c, gate, up, down, stream);
+    return launch_moe_any<Mx4HalfFmt, Mx4HalfFmt>(c, gate, up, down, stream);
 }
 
 }  // namespace mlxq

@@ -330,12 +330,12 @@ __global__ void __launch_bounds__(AsyncSmem<NT>::kThreads, 1) k_mx4_gemm_async(c
                     cp_async_wait<M::kDepth - 2>();
                     __syncwarp();  // the copies of all lanes have landed; the slot refilled below is read out
                     issue();
+                    const uint32_t xs = x0 + static_cast<uint32_t>(stage) * step_bytes;
+                    auto x = [&](int b, int n) { return lds128(xs + static_cast<uint32_t>(b) * piece_stride + xo[n]); };
                     if (NT == 4 && nt <= 2)
-                        F::consume_tiles<MT, NT, (NT + 1) / 2>(p.w, cslot, lane, key, st0 + k, acc, x0 + static_cast<uint32_t>(stage) * step_bytes,
-                                                    piece_stride, xo, plain, field + c0, cols);
+                        F::consume_tiles<MT, NT, (NT + 1) / 2>(p.w, cslot, lane, key, st0 + k, acc, plain, x, FieldUnit{field + c0, cols});
                     else
-                        F::consume_tiles<MT, NT, NT>(p.w, cslot, lane, key, st0 + k, acc, x0 + static_cast<uint32_t>(stage) * step_bytes,
-                                                    piece_stride, xo, plain, field + c0, cols);
+                        F::consume_tiles<MT, NT, NT>(p.w, cslot, lane, key, st0 + k, acc, plain, x, FieldUnit{field + c0, cols});
                     cslot = cslot == ring + M::kRing - M::kStage ? ring : cslot + M::kStage;
                 }
                 __syncwarp();
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(AsyncSmem<NT>::kThreads, 1) k_mx4_gemm_async(c
 #pragma unroll
             for (int j = 0; j < MT; ++j) {
                 const int r0 = tile * kRows + 16 * j;
-                if (plain) F::to_numbers<NT>(acc[j], field + c0, cols, t);
+                if (plain) F::to_numbers<NT>(acc[j], t, FieldUnit{field + c0, cols});
                 if (wk == 1) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)

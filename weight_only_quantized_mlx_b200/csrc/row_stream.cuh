@@ -73,6 +73,13 @@ __device__ __forceinline__ uint32_t x_field(uint32_t field) { return min(max(fie
 __device__ __forceinline__ float x_unit(uint32_t field) { return __uint_as_float((x_field(field) - kXTop) << 23); }
 __device__ __forceinline__ float x_inverse(uint32_t field) { return __uint_as_float((254u + kXTop - x_field(field)) << 23); }  // 1 / unit
 
+// Columns' units from their fields; a column behind the last one has that one's.
+struct FieldUnit {
+    const uint32_t* field;
+    int cols;
+    __device__ __forceinline__ float operator()(int c) const { return x_unit(field[min(c, cols - 1)]); }
+};
+
 // ---- 8-bit group-affine weights: 64 columns per step, 16 codes per lane ------------------
 struct Q8Fmt {
     static constexpr int kStepCols = 64;
@@ -175,7 +182,13 @@ struct Q8Fmt {
         return pack_bf16x2(v.x, v.y);
     }
 
-    static __device__ __forceinline__ int place(int k) { return k; }  // where column k of a row of h is kept
+    // Rows of h, each value the sum of two BF16 parts.  A quad's loads of one piece (lanes t
+    // = 0 .. 3, 16 bytes each) are 64 bytes, the second parts' 64 bytes behind, so that
+    // eight lanes read whole lines.  h_row: length of a row; place: where column k's first part is
+    // (the second: 32 on).
+    static constexpr bool kPair = true;
+    static __host__ __device__ __forceinline__ int h_row(int cols) { return (cols + kStepCols - 1) / kStepCols * (2 * kStepCols); }
+    static __device__ __forceinline__ int place(int k) { return (k & ~63) * 2 + (k >> 3 & 1) * 64 + (k >> 4 & 3) * 8 + (k & 7); }
 
     // shared activations: BF16 as they are; piece r of a step (columns 8r ..) is lane t = r / 2's piece i = r % 2
     static constexpr bool kScaled = false;
@@ -304,8 +317,12 @@ struct Mx4Fmt {
         return (e == 255u ? 0x7FFFu : (e > 128u ? (e - 1u) << 7 : 0x3F80u)) * 0x00010001u;
     }
 
-    // where column k of a row of h is kept: a word of codes comes apart as 0 4 1 5 2 6 3 7
-    static __device__ __forceinline__ int place(int k) { return (k & ~7) | ((k & 3) << 1) | ((k >> 2) & 1); }
+    // rows of h as for 8 bits; and a word of codes comes apart as 0 4 1 5 2 6 3 7
+    static constexpr bool kPair = true;
+    static __host__ __device__ __forceinline__ int h_row(int cols) { return (cols + kStepCols - 1) / kStepCols * (2 * kStepCols); }
+    static __device__ __forceinline__ int place(int k) {
+        return (k & ~127) * 2 + (k >> 3 & 3) * 64 + (k >> 5 & 3) * 8 + ((k & 3) << 1 | (k >> 2 & 1));
+    }
 };
 
 // ---- MX4 weights with shared activations: products in FP16 ---------------------------------
@@ -326,6 +343,9 @@ struct Mx4HalfFmt : Mx4Fmt {
         issue_at(f, slot + static_cast<uint32_t>(g * 64 + ((t ^ (g >> 1)) & 3) * 16), slot + 1024u + static_cast<uint32_t>(lane) * 4u, by);
     }
 
+    // rows of h: FP16 in units of their largest power of two, in order
+    static constexpr bool kPair = false;
+
     static constexpr bool kScaled = true;
     static __device__ __forceinline__ int piece_index(int r) { return r >> 2; }  // block
     static __device__ __forceinline__ int piece_lane(int r) { return r & 3; }
@@ -336,10 +356,10 @@ struct Mx4HalfFmt : Mx4Fmt {
     // does not leave fp32 on the way.
     // MT tiles of 16 rows, their stages one behind the other: each piece of the
     // activations is read once for all of them.
-    template <int MT, int NT, int N>
+    // x(b, n): this lane's piece of block b and column tile n; unit(c): column c's unit.
+    template <int MT, int NT, int N, class X, class Unit>
     static __device__ __forceinline__ void consume_tiles(const Mat& w, uint32_t slot, int lane, const uint32_t (&key)[MT], int step,
-                                                         float (&acc)[MT][NT][4], uint32_t x, uint32_t piece_stride,
-                                                         const uint32_t (&xo)[NT], bool& plain, const uint32_t* field, int cols) {
+                                                         float (&acc)[MT][NT][4], bool& plain, X x, Unit unit) {
         const int g = lane >> 2, t = lane & 3;
         const int left = w.G - 4 * step;  // blocks left in the row; behind it codes are zeros, and scales must not be NaN
         uint32_t ea[MT], eb[MT], mid = 0x80808080u;  // the two top bits of every byte differ: 64 .. 191
@@ -362,7 +382,7 @@ struct Mx4HalfFmt : Mx4Fmt {
         if (plain && !__all_sync(0xFFFFFFFFu, mid == 0x80808080u)) {
             plain = false;
 #pragma unroll
-            for (int j = 0; j < MT; ++j) to_numbers<NT>(acc[j], field, cols, t);
+            for (int j = 0; j < MT; ++j) to_numbers<NT>(acc[j], t, unit);
         }
         float sa[MT][4], sb[MT][4];
 #pragma unroll
@@ -384,7 +404,7 @@ struct Mx4HalfFmt : Mx4Fmt {
                 }
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
-                    const uint4 v = lds128(x + static_cast<uint32_t>(b) * piece_stride + xo[n]);
+                    const uint4 v = x(b, n);
 #pragma unroll
                     for (int j = 0; j < MT; ++j) {
                         float d[4];
@@ -410,13 +430,13 @@ struct Mx4HalfFmt : Mx4Fmt {
                     const float s1 = b == 0 ? sb[j][0] : (b == 1 ? sb[j][1] : (b == 2 ? sb[j][2] : sb[j][3]));
 #pragma unroll
                     for (int n = 0; n < N; ++n) {
-                        const uint4 v = lds128(x + static_cast<uint32_t>(b) * piece_stride + xo[n]);
+                        const uint4 v = x(b, n);
                         float d[4];
                         mma_f16_first(d, a[0], c[0], a[1], c[1], v.x, v.y);
                         mma_f16(d, a[2], c[2], a[3], c[3], v.z, v.w);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float u = x_unit(field[min(n * 8 + 2 * t + (i & 1), cols - 1)]), s = i < 2 ? s0 : s1;
+                            const float u = unit(n * 8 + 2 * t + (i & 1)), s = i < 2 ? s0 : s1;
                             acc[j][n][i] = u <= 1.0f ? __fmaf_rn(d[i] * u, s, acc[j][n][i]) : __fmaf_rn(d[i] * s, u, acc[j][n][i]);
                         }
                     }
@@ -429,16 +449,17 @@ struct Mx4HalfFmt : Mx4Fmt {
                                                           float (&acc)[NT][4], uint32_t x, uint32_t piece_stride,
                                                           const uint32_t (&xo)[NT], bool& plain, const uint32_t* field, int cols) {
         const uint32_t keys[1] = {key};
-        consume_tiles<1, NT, N>(w, slot, lane, keys, step, reinterpret_cast<float(&)[1][NT][4]>(acc), x, piece_stride, xo, plain, field,
-                                cols);
+        consume_tiles<1, NT, N>(
+            w, slot, lane, keys, step, reinterpret_cast<float(&)[1][NT][4]>(acc), plain,
+            [&](int b, int n) { return lds128(x + static_cast<uint32_t>(b) * piece_stride + xo[n]); }, FieldUnit{field, cols});
     }
 
-    template <int NT>
-    static __device__ __forceinline__ void to_numbers(float (&acc)[NT][4], const uint32_t* field, int cols, int t) {
+    template <int NT, class Unit>
+    static __device__ __forceinline__ void to_numbers(float (&acc)[NT][4], int t, Unit unit) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] *= x_unit(field[min(n * 8 + 2 * t + (i & 1), cols - 1)]);
+            for (int i = 0; i < 4; ++i) acc[n][i] *= unit(n * 8 + 2 * t + (i & 1));
     }
 
     static __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
@@ -720,7 +741,7 @@ __device__ __forceinline__ void shared_phase(const Job& job, uint32_t ring, uint
                 else run(std::integral_constant<int, 8>{});
             }
             if constexpr (F::kScaled) {
-                if (plain) F::template to_numbers<NT>(acc, xb.field, cols, t);
+                if (plain) F::template to_numbers<NT>(acc, t, FieldUnit{xb.field, cols});
             }
             if (wk == 1) {
                 if (live) {
