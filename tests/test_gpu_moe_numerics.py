@@ -77,3 +77,43 @@ def test_h_is_held_to_eleven_bits(m, k, group):
     assert (off <= slack + 2.0 ** -8 * (want.abs() + slack)).all()
     # y's rounding: at most 2^-8, 2^-8 / sqrt(3) in the mean; h's the same with 2^-11
     assert float(off.norm() / want.norm()) <= math.hypot(2.0 ** -8, 2.0 ** -11) / math.sqrt(3)
+
+
+def routed(L, choices):
+    """Activations that send token t to the experts choices[t] (the first E columns are the router's)."""
+    m, E = len(choices), L.E
+    L.router.zero_()
+    L.router[:, :E] = 8 * torch.eye(E, device="cuda")
+    x = dev(synth.activations(L.g, m, L.H))
+    x[:, :E] = 0
+    for t, experts in enumerate(choices):
+        x[t, list(experts)] = 8.0
+    return x
+
+
+# tokens of the bad expert, of the one behind it, and of all; choices of a token
+@pytest.mark.parametrize("bad,behind,m,k", [(9, 16, 16, 2), (11, 32, 64, 1), (17, 32, 64, 1), (20, 32, 64, 1), (24, 31, 64, 1),
+                                            (28, 32, 64, 1), (3, 7, 8, 2)])
+@pytest.mark.parametrize("group", [64, 0], ids=["gs64", "mx4"])
+def test_a_bad_expert_ahead_of_a_fuller_one(bad, behind, m, k, group):
+    """A NaN expert whose tokens do not fill its column tiles, followed by one with more: three hit
+    experts of 64 steps, so that every warp of the down phase walks through all of them."""
+    E, H, I = 3, 64, 4096 if group else 8192
+    L = Layer(60, E, H, I, group)
+    if k == 1:
+        choices = [(0,) if t < bad else (1,) if t < bad + behind else (2,) for t in range(m)]
+    else:  # the first tokens choose expert 0, the last ones expert 1, and all that are left expert 2
+        choices = [tuple((([0] if t < bad else []) + ([1] if t >= m - behind else []) + [2])[:2]) for t in range(m)]
+    x = routed(L, choices)
+    clean = L.run(x, k)
+    assert torch.isfinite(clean.float()).all()
+    if group:
+        L.keep[2][1][:H] = float("nan")
+    else:
+        L.handles[2].tensors[1][:H] = 255
+    y = L.run(x, k)
+    for t in range(m):
+        if 0 in choices[t]:
+            assert not torch.isfinite(y[t].float()).any(), t
+        else:
+            assert torch.equal(y[t], clean[t]), t

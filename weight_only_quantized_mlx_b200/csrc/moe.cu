@@ -610,8 +610,10 @@ __device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L
                             }
                         }
                     }
-                    acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
                 }
+                // all tiles: an unused one that was multiplied holds zeros times weights, NaN where they are infinite
+#pragma unroll
+                for (int n = 0; n < DT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
                 __syncwarp();
             };
             auto column = [&](int a, int n) {
