@@ -117,3 +117,21 @@ def test_a_bad_expert_ahead_of_a_fuller_one(bad, behind, m, k, group):
             assert not torch.isfinite(y[t].float()).any(), t
         else:
             assert torch.equal(y[t], clean[t]), t
+
+
+@pytest.mark.parametrize("E", [2, 9, 12, 15, 20, 36, 68, 130])
+@pytest.mark.parametrize("m", [1, 20, 40])
+def test_equal_router_rows_take_the_lowest_experts(E, m):
+    """Equal rows that are not zero: an expert's logit does not depend on the block that sums it."""
+    H, I, k = 4096, 32, min(E, 3)
+    L = Layer(70, 1, H, I, 0)
+    g = synth.rng(70 + E)
+    weights = [mq.mx4_view(*(torch.cat([t] * E) for t in h.tensors)) for h in L.handles]  # E times the same expert
+    weights[2].tensors[1].view(E, -1)[k:] = 255  # but for NaN where another than the lowest k is chosen
+    ws = torch.empty(mq.mlxq_moe_workspace_bytes(H, I, k, m), dtype=torch.uint8, device="cuda")
+    for _ in range(6):
+        router = dev(np.repeat(synth.to_bf16_bits(g.standard_normal((1, H)) / 16), E, axis=0))
+        x = dev(synth.activations(g, m, H))
+        y = torch.empty(m, H, dtype=torch.bfloat16, device="cuda")
+        mq.mlxq_mx4_moe(router, *weights, E, k, x, y, m, ws)
+        assert torch.isfinite(y.float()).all()

@@ -116,9 +116,11 @@ __global__ void __cluster_dims__(kRouterCluster, 1, 1) __launch_bounds__(kRouter
     const int t0 = (blockIdx.x / kRouterCluster) * TB;
     auto started = cluster.barrier_arrive();  // waited for before the first write to the root's memory
     pdl_wait();
-    // experts rank, rank + 8, ...; with fewer of them than warps, several warps share one's H
+    // experts rank, rank + 8, ...; with fewer of them than warps, several warps share one's H.
+    // As many for every expert of the call: equal rows have equal sums, whose block's they are.
     const int mine = p.E > rank ? (p.E - rank - 1) / kRouterCluster + 1 : 0;
-    const int split = mine > 8 ? 1 : (mine > 4 ? 2 : (mine > 2 ? 4 : (mine > 1 ? 8 : 16)));
+    const int most = (p.E + kRouterCluster - 1) / kRouterCluster;
+    const int split = most > 8 ? 1 : (most > 4 ? 2 : (most > 2 ? 4 : (most > 1 ? 8 : 16)));
     const int sub = warp % split, chunks = p.H / 8;
     for (int i = warp / split; i < mine; i += kRouterWarps / split) {
         const uint4* r = reinterpret_cast<const uint4*>(p.router + static_cast<int64_t>(rank + kRouterCluster * i) * p.H);
