@@ -54,11 +54,15 @@ EXPORTS = ("mlxq_load", "mlxq_dequant", "mlxq_gemv", "mlxq_gemv_silu_gate",
 
 
 class mlxq_weight(ctypes.Structure):
-    """C ``mlxq_weight``: three device pointers and the dimensions."""
+    """C ``mlxq_weight``: three device pointers and the dimensions.  A handle made by
+    :func:`weight_view` keeps its tensors alive (``tensors``); ``problem`` says why
+    they are not a whole weight, where they are not."""
     _fields_ = [("packed", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("biases", ctypes.c_void_p), ("out_features", ctypes.c_uint32),
                 ("in_features", ctypes.c_uint32), ("group_size", ctypes.c_uint32),
                 ("flags", ctypes.c_uint32)]
+    tensors = None
+    problem = None
 
 
 class mlxq_mx4(ctypes.Structure):
@@ -200,6 +204,16 @@ def _mx4(h: mlxq_mx4, name: str, device: int):
     return ctypes.byref(h)
 
 
+def _q8(h: mlxq_weight, name: str, device: int):
+    """The same for an 8-bit handle."""
+    if h.tensors is not None:
+        if h.problem is not None:
+            raise MlxqError(MLXQ_ERR_INVALID_ARG, f"{name}: {h.problem}")
+        if h.tensors[0].get_device() != device:
+            _local(h.tensors[0], name, device)
+    return ctypes.byref(h)
+
+
 def _check(rc: int) -> None:
     if rc != MLXQ_OK:
         raise MlxqError(rc, mlxq_last_error())
@@ -276,7 +290,26 @@ def weight_view(packed, scales, biases, group_size: int, flags: int = 0) -> mlxq
     [N, K/4], scales/biases bf16 [N, K/gs]).  Never pass it to mlxq_release."""
     N = packed.shape[0]
     K = packed.shape[1] * 4
-    return mlxq_weight(_ptr(packed), _ptr(scales), _ptr(biases), N, K, group_size, flags)
+    h = mlxq_weight(_ptr(packed), _ptr(scales), _ptr(biases), N, K, group_size, flags)
+    tensors = (packed, scales, biases)
+    if all(hasattr(t, "get_device") for t in tensors):
+        h.tensors = tensors
+        h.problem = _weight_problem(packed, scales, biases, group_size)
+    return h
+
+
+def _weight_problem(packed, scales, biases, group_size: int):
+    """Why tensors are not a contiguous weight in one place (None: they are)."""
+    if not all(t.is_contiguous() for t in (packed, scales, biases)):
+        return "packed, scales and biases must be contiguous"
+    if packed.dim() != 2 or packed.element_size() != 4:
+        return f"packed must be 32-bit [N, K/4], got {packed.dtype} {tuple(packed.shape)}"
+    for t in (scales, biases):
+        if str(t.dtype) != "torch.bfloat16" or t.numel() * group_size != packed.numel() * 4:
+            return f"scales and biases must be bfloat16 [N, K/{group_size}], got {t.dtype} {tuple(t.shape)}"
+        if t.device != packed.device:
+            return f"packed is on {packed.device} and its tables on {t.device}"
+    return None
 
 
 def mx4_view(codes, scales) -> mlxq_mx4:
@@ -346,8 +379,9 @@ def _moe(fn, hidden, router, weights, experts, top_k, x, y, m, workspace, stream
 def mlxq_moe(router, gate: mlxq_weight, up: mlxq_weight, down: mlxq_weight, experts: int, top_k: int, x, y, m: int,
              workspace, stream=None, flags: int = 0) -> None:
     """workspace: a device tensor of at least mlxq_moe_workspace_bytes(...) bytes, for one call at a time."""
-    weights = [ctypes.byref(h) for h in (gate, up, down)]
-    _moe(lib().mlxq_moe, gate.in_features, router, weights, experts, top_k, x, y, m, workspace, stream, flags, _device())
+    d = _device()
+    weights = [_q8(gate, "gate", d), _q8(up, "up", d), _q8(down, "down", d)]
+    _moe(lib().mlxq_moe, gate.in_features, router, weights, experts, top_k, x, y, m, workspace, stream, flags, d)
 
 
 def mlxq_mx4_moe(router, gate: mlxq_mx4, up: mlxq_mx4, down: mlxq_mx4, experts: int, top_k: int, x, y, m: int,
