@@ -135,3 +135,34 @@ def test_equal_router_rows_take_the_lowest_experts(E, m):
         y = torch.empty(m, H, dtype=torch.bfloat16, device="cuda")
         mq.mlxq_mx4_moe(router, *weights, E, k, x, y, m, ws)
         assert torch.isfinite(y.float()).all()
+
+
+@pytest.mark.parametrize("low,high", [(250, 255), (0, 255), (124, 134)])
+@pytest.mark.parametrize("m", [1, 4, 7, 40])
+def test_down_scales_at_the_ends_of_the_range(m, low, high):
+    """Down weights up to 6 * 2^127, beyond BF16 and fp32, times an h so small that the products are not."""
+    E, H, I, k = 4, 96, 288, 2
+    L = Layer(80, E, H, I, 0)
+    L.handles, L.values = [], []
+    # h near 2^-110: the up weights are that small
+    for rows, cols, ends in ((E * I, H, (121, 124)), (E * I, H, (14, 17)), (E * H, I, (low, high))):
+        codes, scales = ref.random_weight(L.g, rows, cols, *ends)
+        L.handles.append(mq.mx4_view(dev(ref.pack(codes)), dev(scales)))
+        L.values.append(torch.from_numpy(ref.values(codes, scales)).cuda().reshape(E, -1, cols))
+    xb = synth.activations(L.g, m, H)
+    want, _, err = L.reference(xb, k)
+    assert torch.isfinite(want).all()
+    y = L.run(dev(xb), k).double()
+    # (2^-133: the last place of a BF16 result below 2^-126; a BF16 part below it is off by up to 2^-134)
+    small = 2.0 ** -133 + sum(2.0 ** -134 * v.abs().sum(-1).amax(0) for v in [L.values[2]]) * k
+    assert torch.isfinite(y).all() and ((y - want).abs() <= err + small).all()
+
+
+@pytest.mark.parametrize("m", [2, 9])
+def test_no_product_times_the_largest_scales_is_zero(m):
+    """h = 0 times the largest down weights: zero, not NaN."""
+    E, H, I, k = 2, 64, 64, 1
+    L = Layer(81, E, H, I, 0)
+    L.handles[1].tensors[0].zero_()  # up
+    L.handles[2].tensors[1].fill_(254)
+    assert not L.run(dev(synth.activations(L.g, m, H)), k).any()

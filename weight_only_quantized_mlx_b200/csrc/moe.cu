@@ -598,8 +598,8 @@ __device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L
                         const int s = cm.slot(a, n * 4 + t);
                         if (s >= 0) {
                             const int token = s / cm.top_k;
-                            area[g * kStride + token] += acc[n][0] + acc[n][1];
-                            area[(g + 8) * kStride + token] += acc[n][2] + acc[n][3];
+                            area[g * kStride + token] += F::kUnit * (acc[n][0] + acc[n][1]);
+                            area[(g + 8) * kStride + token] += F::kUnit * (acc[n][2] + acc[n][3]);
                         }
                     } else {
 #pragma unroll
@@ -700,8 +700,8 @@ __device__ __forceinline__ void down_phase(const Params& p, const ExpertLists& L
                     for (int i = 0; i < 2; ++i) {
                         const int n = F::kPair ? i : 0;
                         if (cm.slot(a, F::kPair ? 4 * i + t : 2 * t + i) < 0) continue;
-                        sum[2 * i] += F::kPair ? acc[n][0] + acc[n][1] : acc[n][i];
-                        sum[2 * i + 1] += F::kPair ? acc[n][2] + acc[n][3] : acc[n][2 + i];
+                        sum[2 * i] += F::kPair ? F::kUnit * (acc[n][0] + acc[n][1]) : acc[n][i];
+                        sum[2 * i + 1] += F::kPair ? F::kUnit * (acc[n][2] + acc[n][3]) : acc[n][2 + i];
                     }
 #pragma unroll
                     for (int n = 0; n < DT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;

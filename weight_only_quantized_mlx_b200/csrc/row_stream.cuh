@@ -140,7 +140,8 @@ struct Q8Fmt {
     // What a lane needs to read its scales: the parity of its row's first entry.
     static __device__ __forceinline__ uint32_t row_key(const Mat& w, uint32_t row) { return row & static_cast<uint32_t>(w.G) & 1u; }
 
-    // One step: acc[n] += W(16 rows) x(8 columns n), n < N, over the step's k.
+    // One step: acc[n] += W(16 rows) x(8 columns n) / kUnit, n < N, over the step's k.
+    static constexpr float kUnit = 1.f;
     // x(i, n): this lane's piece i of column tile n.
     template <int NT, int N, class X>
     static __device__ __forceinline__ void consume(const Mat& w, uint32_t slot, int lane, uint32_t key, int step,
@@ -276,7 +277,7 @@ struct Mx4Fmt {
         uint32_t ea = (__funnelshift_r(tb.x, tb.y, key) >> (8 * t)) & 255u;
         uint32_t eb = (__funnelshift_r(tb.z, tb.w, key) >> (8 * t)) & 255u;
         if (!in) ea = eb = 0u;  // codes there are zeros; another row's scale must not make them NaN
-        // W = code 2^-126 * 2^(E - 1): one exact product while E <= 128 (scales up
+        // W / 4 = code 2^-126 * 2^(E - 3): one exact product while E <= 128 (scales up
         // to 2); larger scales (and NaN) take a second factor
         const bool big = __any_sync(0xFFFFFFFFu, max(ea, eb) > 128u);
         const uint32_t fa = scale_factor(ea), fb = scale_factor(eb);
@@ -309,9 +310,12 @@ struct Mx4Fmt {
         }
     }
 
-    // 2^(min(E, 128) - 1), twice: exponent field min(E, 128) + 126 (at most 254);
-    // E = 0 is field 126 as well as 2^-127 * 2^126 = 1/2 asks.
-    static __device__ __forceinline__ uint32_t scale_factor(uint32_t e) { return ((min(e, 128u) + 126u) << 7) * 0x00010001u; }
+    // Weights are multiplied as W / kUnit: 6 * 2^127 is beyond BF16 where its product
+    // with x need not be (and a quarter of the least, 2^-130, BF16 still holds).
+    static constexpr float kUnit = 4.f;
+    // 2^(min(E, 128) - 3), twice: exponent field min(E, 128) + 124; E = 0 is field 124
+    // as well as 2^-127 * 2^126 / 4 = 1/8 asks.
+    static __device__ __forceinline__ uint32_t scale_factor(uint32_t e) { return ((min(e, 128u) + 124u) << 7) * 0x00010001u; }
     // the rest: 2^(E - 128) for E > 128, NaN for 255, else 1
     static __device__ __forceinline__ uint32_t scale_rest(uint32_t e) {
         return (e == 255u ? 0x7FFFu : (e > 128u ? (e - 1u) << 7 : 0x3F80u)) * 0x00010001u;
