@@ -62,3 +62,25 @@ def test_a_view_keeps_its_tensors():
     ref = weakref.ref(h.tensors[1])
     gc.collect()
     assert ref() is not None and h.scales == ref().data_ptr()
+
+
+def test_numbers_past_32_bits_are_refused(called, monkeypatch):
+    """The C side's numbers are 32 bits wide: what does not fit must not come out as another number."""
+    big = 2 ** 32 + 64
+    meta = lambda *s: torch.empty(*s, dtype=torch.int32, device="meta")
+    bytes_ = lambda *s: torch.empty(*s, dtype=torch.uint8, device="meta")
+    assert code_of(mq.mx4_view, meta(big, 4), bytes_(big, 1)) == mq.MLXQ_ERR_SHAPE
+    assert code_of(mq.mx4_view, meta(1, big // 8), bytes_(1, big // 32)) == mq.MLXQ_ERR_SHAPE
+    wide = torch.empty(2 ** 32 + 1, 1, dtype=torch.bfloat16, device="meta")
+    tall = mq.weight_view(meta(2 ** 32 + 1, 16), wide, wide, 64)
+    assert tall.problem is not None
+    for kw in (dict(m=2 ** 32 + 3), dict(m=-1), dict(top_k=2 ** 32 + 2), dict(experts=2 ** 32 + E), dict(flags=2 ** 32)):
+        assert code_of(lambda: moe8(**kw)) == mq.MLXQ_ERR_INVALID_ARG, kw
+    assert not called
+
+
+def test_mx4_gemm_rows_past_32_bits_are_refused():
+    for m in (2 ** 32, 2 ** 32 + 1, -(2 ** 32) + 1):
+        assert code_of(mq.mlxq_mx4_gemm, mq.mlxq_mx4(1 << 20, 2 << 20, 64, 64), 4 << 20, 8 << 20, m, 0) == mq.MLXQ_ERR_INVALID_ARG
+    for args in ((2 ** 32 + 64, 64, 2, 2), (64, 2 ** 32 + 64, 2, 2), (64, 64, 2 ** 32 + 2, 2), (64, 64, 2, 2 ** 32 + 2), (64, 64, 2, -1)):
+        assert mq.mlxq_moe_workspace_bytes(*args) == 0

@@ -197,6 +197,13 @@ def _dense(b, name: str, elems: int, device: int):
     return b.data_ptr()
 
 
+def _fits(**numbers) -> None:
+    """Refuse numbers that 32 bits do not hold: ctypes would cut them to others."""
+    for name, v in numbers.items():
+        if not 0 <= v <= 0xFFFFFFFF:
+            raise MlxqError(MLXQ_ERR_INVALID_ARG, f"{name} is out of range: {v}")
+
+
 def _mx4(h: mlxq_mx4, name: str, device: int):
     """A handle as an argument of a call; its tensors, where it has any, are on the current device."""
     if h.tensors is not None and h.tensors[0].get_device() != device:
@@ -304,6 +311,8 @@ def _weight_problem(packed, scales, biases, group_size: int):
         return "packed, scales and biases must be contiguous"
     if packed.dim() != 2 or packed.element_size() != 4:
         return f"packed must be 32-bit [N, K/4], got {packed.dtype} {tuple(packed.shape)}"
+    if max(packed.shape[0], packed.shape[1] * 4) > 0xFFFFFFFF:
+        return f"dimensions must fit 32 bits, got {packed.shape[0]} x {packed.shape[1] * 4}"
     for t in (scales, biases):
         if str(t.dtype) != "torch.bfloat16" or t.numel() * group_size != packed.numel() * 4:
             return f"scales and biases must be bfloat16 [N, K/{group_size}], got {t.dtype} {tuple(t.shape)}"
@@ -321,6 +330,8 @@ def mx4_view(codes, scales) -> mlxq_mx4:
                                         f"{tuple(codes.shape)} and {tuple(scales.shape)}")
     if not codes.is_contiguous() or not scales.is_contiguous():
         raise MlxqError(MLXQ_ERR_INVALID_ARG, "MX4 codes and scales must be contiguous")
+    if max(codes.shape[0], codes.shape[1] * 8) > 0xFFFFFFFF:
+        raise MlxqError(MLXQ_ERR_SHAPE, f"MX4 dimensions must fit 32 bits, got {codes.shape[0]} x {codes.shape[1] * 8}")
     if codes.device != scales.device:
         raise MlxqError(MLXQ_ERR_INVALID_ARG, f"MX4 codes are on {codes.device} and scales on {scales.device}")
     h = mlxq_mx4(_ptr(codes), _ptr(scales), codes.shape[0], codes.shape[1] * 8)
@@ -351,6 +362,7 @@ def mlxq_mx4_dequant(w: mlxq_mx4, out, stream=None) -> None:
 
 def mlxq_mx4_gemm(w: mlxq_mx4, x, y, m: int, stream=None) -> None:
     d = _device()
+    _fits(m=m)
     x, y = _dense(x, "X", m * w.cols, d), _dense(y, "Y", m * w.rows, d)
     _check(lib().mlxq_mx4_gemm(_mx4(w, "w", d), x, y, m, _stream(stream, d)))
 
@@ -362,10 +374,13 @@ def mlxq_mx4_matmul(w: mlxq_mx4, a: mlxq_mx4, y, stream=None) -> None:
 
 
 def mlxq_moe_workspace_bytes(hidden: int, inter: int, top_k: int, m: int) -> int:
+    if not all(0 <= v <= 0xFFFFFFFF for v in (hidden, inter, top_k, m)):
+        return 0
     return lib().mlxq_moe_workspace_bytes(hidden, inter, top_k, m)
 
 
 def _moe(fn, hidden, router, weights, experts, top_k, x, y, m, workspace, stream, flags, d):
+    _fits(experts=experts, top_k=top_k, m=m, flags=flags)
     router = _dense(router, "router", experts * hidden, d)
     x, y = _dense(x, "x", m * hidden, d), _dense(y, "y", m * hidden, d)
     if not hasattr(workspace, "data_ptr") or not workspace.is_contiguous():
