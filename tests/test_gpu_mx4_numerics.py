@@ -49,3 +49,43 @@ def test_gemm_activations_far_below_their_rows_largest(m, K, least):
     small[:, top] = 0  # products with zero codes are zero
     err = np.abs(bits_to_f64(host_bits(y)) - want)
     assert np.all(err <= bound(np.abs(w), np.abs(small) + 2.0 ** -39 * largest, want, K) + lost + 2.0 ** -8 * lost)
+
+
+@pytest.mark.parametrize("m", [1, 8, 20])
+@pytest.mark.parametrize("byte", [0, 3, 40])
+@pytest.mark.parametrize("top", [127, 60, 20])
+def test_gemm_least_scales_with_large_activations(m, byte, top):
+    """Scales down to 2^-127 with activations up to 2^127, the largest under zero codes: the small ones' products
+    with the scale alone would be fp32 subnormals."""
+    N, K = 400, 32  # few terms: the bound leaves little
+    g, codes, scales, _ = make(41, N, K)
+    codes[:, 7] = 0
+    scales[:] = byte + g.integers(0, 2, scales.shape)
+    h = mq.mx4_view(dev(ref.pack(codes)), dev(scales))
+    w = ref.values(codes, scales)
+    v = g.uniform(1, 1.9, (m, K)) * np.sign(g.standard_normal((m, K))) * 2.0 ** (top - 30)
+    v[:, 7] = 1.5 * 2.0 ** top
+    xb = synth.to_bf16_bits(v)
+    x = bits_to_f64(xb)
+    y = torch.empty(m, N, dtype=torch.bfloat16, device="cuda")
+    mq.mlxq_mx4_gemm(h, dev(xb), y, m)
+    want = x @ w.T
+    x[:, 7] = 0
+    err = np.abs(bits_to_f64(host_bits(y)) - want)
+    # (2^-133: the last place of a BF16 result below 2^-126)
+    assert np.all(err <= bound(np.abs(w), np.abs(x), want, K) + 2.0 ** -133)
+
+
+@pytest.mark.parametrize("wlow,alow", [(0, 235), (235, 0), (60, 60), (160, 160), (100, 150)])
+@pytest.mark.parametrize("m,N,K", [(20, 300, 544), (300, 520, 512)])
+def test_matmul_scales_at_the_ends_of_the_range(m, N, K, wlow, alow):
+    """Scales of both operands from 2^-127 to 2^127 whose products fp32 holds."""
+    g, wc, ws, w = make(42, N, K, low=wlow, high=wlow + 20)
+    ac, as_ = ref.random_weight(g, m, K, low=alow, high=alow + 20)
+    y = torch.empty(m, N, dtype=torch.bfloat16, device="cuda")
+    mq.mlxq_mx4_matmul(w, mq.mx4_view(dev(ref.pack(ac)), dev(as_)), y)
+    wv, av = ref.values(wc, ws), ref.values(ac, as_)
+    want = av @ wv.T
+    err = np.abs(bits_to_f64(host_bits(y)) - want)
+    # (2^-133: the last place of a BF16 result below 2^-126; 2^-149: fp32's)
+    assert np.all(err <= bound(np.abs(wv), np.abs(av), want, K) + 2.0 ** -133 + K * 2.0 ** -149)

@@ -441,7 +441,9 @@ struct Mx4HalfFmt : Mx4Fmt {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const float u = unit(n * 8 + 2 * t + (i & 1)), s = i < 2 ? s0 : s1;
-                            acc[j][n][i] = u <= 1.0f ? __fmaf_rn(d[i] * u, s, acc[j][n][i]) : __fmaf_rn(d[i] * s, u, acc[j][n][i]);
+                            // a large and a small one are exact together; two of a side might leave fp32
+                            const bool same = (u >= 1.0f) == (s >= 1.0f);
+                            acc[j][n][i] = __fmaf_rn(same ? d[i] * u : d[i], same ? s : s * u, acc[j][n][i]);
                         }
                     }
                 }
