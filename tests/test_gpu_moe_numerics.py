@@ -166,3 +166,29 @@ def test_no_product_times_the_largest_scales_is_zero(m):
     L.handles[1].tensors[0].zero_()  # up
     L.handles[2].tensors[1].fill_(254)
     assert not L.run(dev(synth.activations(L.g, m, H)), k).any()
+
+
+@pytest.mark.parametrize("group", [64, 0], ids=["gs64", "mx4"])
+@pytest.mark.parametrize("m", [3, 6, 20, 64])
+def test_tokens_of_very_different_sizes(m, group):
+    """Each slot's h has a size of its own, from 2^-40 to 2^40 of the others."""
+    E, H, I, k = 5, 128, 192, 2
+    L = Layer(90, E, H, I, group)
+    x32 = synth.bf16_bits_to_f32(synth.activations(L.g, m, H)) * np.float32(2.0) ** L.g.integers(-20, 21, (m, 1)).astype(np.float32)
+    xb = synth.to_bf16_bits(x32)
+    want, _, err = L.reference(xb, k)
+    y = L.run(dev(xb), k).double()
+    assert torch.isfinite(y).all() and ((y - want).abs() <= err).all()
+
+
+@pytest.mark.parametrize("m", [6, 24])
+@pytest.mark.parametrize("bad", [0x7FC0, 0x7F80])
+@pytest.mark.parametrize("group", [64, 0], ids=["gs64", "mx4"])
+def test_a_bad_token_leaves_the_others_bits(m, bad, group):
+    L = Layer(91, 6, 128, 160 if group == 0 else 128, group)
+    xb = synth.activations(L.g, m, 128)
+    clean = L.run(dev(xb), 2)
+    xb[2, 9] = bad
+    y = L.run(dev(xb), 2)
+    keep = [t for t in range(m) if t != 2]
+    assert torch.equal(y[keep], clean[keep]) and not torch.isfinite(y[2].float()).any()

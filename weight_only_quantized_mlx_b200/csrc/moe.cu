@@ -11,17 +11,20 @@
 // builds the lists of tokens per expert, then streams its share of the hit
 // experts' gate and up rows (row_stream.cuh; the 16 rows of a tile are 8 gate
 // rows and the same 8 up rows, so silu(gate) * up is a lane's own business),
-// writes h, crosses a grid barrier, and streams its share of the down rows over
-// all experts at once.  Each weight byte of a hit expert is read once (again for every
-// 8 NT tokens more of one expert).  The ring is filled with down rows
-// before the barrier, so the barrier's wait overlaps their copies.
+// writes h, crosses a grid barrier (two, with a conversion of h between them, in one
+// form: see Rounding), and streams its share of the down rows over all experts at
+// once.  Each weight byte of a hit expert is read once (again for every 8 NT tokens
+// more of one expert).  The ring is filled with down rows before the barrier, so the
+// barrier's wait overlaps their copies.
 //
-// Measured: one token, two of 8 experts of 4096 x 14336, 8 bits: 107 us (the
-// weights' copy time is 57); 64 tokens, 128 experts of 4128 x 1504, MX4: 485 us
-// (190).  The warps' instructions bound both (issue slots 63 % filled), most of them
-// for turning codes into operands.  One token, 8 of 64 experts of 2048 x 1024, MX4:
-// 25 us (4), a chain of latencies: router 5 us, lists 1.4, first copies and
-// activations 2.3, gate and up 5, barrier 3.5, down 4.2.
+// Measured: one token, two of 8 experts of 4096 x 14336, 8 bits: 108 us (the
+// weights' copy time is 57); 64 tokens, 128 experts of 4128 x 1504, MX4: 465 us
+// (190).  Neither fills a unit (issue slots 63 and 59 %, ALU 62 and 52 %, DRAM 43 and
+// 36 %): the four warps of a scheduler mostly wait for their own instructions' results
+// and for one another, most of the instructions turning codes into operands.  One
+// token, 8 of 64 experts of 2048 x 1024, MX4: 25 us (4), a chain of latencies: router
+// 5 us, lists 1.4, first copies and activations 2.3, gate and up 5, barrier 3.5, down
+// 4.2.
 //
 // Rounding: the tensor pipe takes 16-bit operands, and one BF16 value for h (with p in
 // it) showed in y (relative error 2.4e-3 against 1.7e-3 of y's own rounding).  So h is
@@ -832,7 +835,8 @@ cudaError_t launch_moe(const MoeCall& c, const WeightView& gate, const WeightVie
 cudaError_t launch_mx4_moe(const MoeCall& c, const Mx4View& gate, const Mx4View& up, const Mx4View& down,
                            cudaStream_t stream) {
     // Up to four tokens fit a column tile with both parts of h, which needs no second
-    // barrier and no pass over h in between (about 3 us).
+    // barrier and no pass over h in between: 24.9 against 26.6 us at one token (8 of 64
+    // experts of 2048 x 1024), 47.2 against 47.3 at four; at eight 72 against 63.
     if (c.m <= 4) return launch_both<Mx4HalfFmt, Mx4Fmt, 1>(c, gate, up, down, stream);
     return launch_moe_any<Mx4HalfFmt, Mx4HalfFmt>(c, gate, up, down, stream);
 }

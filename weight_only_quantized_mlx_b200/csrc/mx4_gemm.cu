@@ -5,10 +5,10 @@
 //
 // k_mx4_gemm, up to 8 rows of X: a block keeps them in shared memory, converted on
 // the way (in chunks of K where they do not fit).  28672 x 8192, one row: 39 us, 3.2
-// TB/s of the weight, half of the measured copy rate; the warps' instructions bound
-// it (issue slots 64 % filled; turning codes into FP16 alone takes about half the
-// time that the weight needs from HBM).  4096 x 4096: 7.3 us, mostly the latencies of
-// one launch, of the first loads and of the join.
+// TB/s of the weight, half of the measured copy rate.  No unit is full (issue slots 64
+// %, ALU 51 %, tensor pipe 20 %, DRAM 36 %): three warps a scheduler wait for their own
+// instructions' results.  4096 x 4096: 7.3 us, mostly the latencies of one launch,
+// of the first loads and of the join.
 //
 // k_mx4_gemm_async, more rows: every block needs all of X over its columns, and
 // fetching and converting them between products took most of the time (4096 x
@@ -17,9 +17,11 @@
 // a ring while the warps multiply.  Where rows are few, four blocks of a cluster share
 // a range of rows and split K, which divides the copies of X, and add their sums
 // through distributed shared memory in rank order.  28672 x 8192: 16 rows 65 us, 32
-// rows 92, 64 rows 171; 4096 x 4096: 14, 16, 19.  The products bound it (without
+// rows 92, 64 rows 171; 4096 x 4096: 14, 16, 19.  The products take the time (without
 // them 33 us whatever the rows at 28672 x 8192; without the copies of the weight 64,
-// 93 and 145).
+// 93 and 145), and again no unit is full (64 rows: issue slots 42 %, tensor pipe 38 %,
+// DRAM 9 %; two warps a scheduler, which wait for their own results).  The 8-bit gemm of
+// this library takes 76, 101 and 120 us there: from 40 rows on it is the faster one.
 #include <cooperative_groups.h>
 
 #include "row_stream.cuh"
